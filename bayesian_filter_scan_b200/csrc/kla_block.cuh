@@ -1,0 +1,182 @@
+// kla_block.cuh -- shared definitions of the recurrent block's kernels: short
+// convolution, selective scan, layer norm (sm_100a).
+#pragma once
+
+#include <type_traits>
+
+#include "kla_internal.cuh"
+
+namespace kla {
+
+// The sequences on the token axis: B rows of T tokens, or packed offsets.
+struct SeqAxis {
+    long long ntok, T;
+    const int *cu;
+    int nseq;
+
+    // Tokens [s0, s1) of sequence n. Offsets are clamped to the axis, so a bad
+    // offset cannot lead outside the tensors.
+    __device__ __forceinline__ void range(int n, long long &s0, long long &s1) const {
+        if (!cu) {
+            s0 = n * T;
+            s1 = s0 + T;
+            return;
+        }
+        s0 = min(max((long long)cu[n], 0LL), ntok);
+        s1 = min(max((long long)cu[n + 1], s0), ntok);
+    }
+    // The sequence that holds token t, or -1. Of several that start at the same
+    // token the last one holds it: the others are empty.
+    __device__ __forceinline__ int find(long long t) const {
+        if (!cu) return (int)(t / T);
+        if (t < cu[0] || t >= cu[nseq]) return -1;
+        int lo = 0, hi = nseq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        return lo;
+    }
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V contiguous values as floats: one access of V * sizeof(T) = 8 or 16 bytes, or V is 1.
+template <int V, typename T>
+__device__ __forceinline__ void load_v(const T *p, float (&x)[V]) {
+    if constexpr (V == 1) {
+        x[0] = to_f(*p);
+    } else {
+        constexpr int K = V * (int)sizeof(T) / 4;
+        static_assert(K == 2 || K == 4, "one 8- or 16-byte access");
+        uint32_t w[K];
+        if constexpr (K == 4) {
+            const uint4 r = *reinterpret_cast<const uint4 *>(p);
+            w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+        } else {
+            const uint2 r = *reinterpret_cast<const uint2 *>(p);
+            w[0] = r.x; w[1] = r.y;
+        }
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+template <int V, typename T>
+__device__ __forceinline__ void store_v(T *p, const float (&x)[V]) {
+    if constexpr (V == 1) {
+        *p = from_f<T>(x[0]);
+    } else {
+        constexpr int K = V * (int)sizeof(T) / 4;
+        static_assert(K == 2 || K == 4, "one 8- or 16-byte access");
+        uint32_t w[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                w[i] = __float_as_uint(x[i]);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        if constexpr (K == 4) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+}
+
+// Sigmoid through the accurate exponential; saturates without NaN.
+__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+
+// Sums part[rows][cols] over its rows in a fixed order: the first n0 columns go
+// to out0, the next n1 to out1, the others to out2; a NULL output is skipped
+// (kla_block_api.cu).
+cudaError_t launch_colsum(const float *part, long long rows, long long cols, long long n0, float *out0, long long n1,
+                          float *out1, float *out2, cudaStream_t st);
+
+// ---- launch functions behind the C ABI ------------------------------------------
+
+struct ConvArgs {
+    SeqAxis ax;
+    int D, W;
+    bool silu;
+    long long ld_x;
+    const void *x;
+    const float *w, *bias;
+    const void *state0;
+    void *out, *final_state;
+    // backward
+    const void *dout, *dfinal;
+    void *dx, *dstate0;
+    float *part;       // [blocks][D*W taps, then D biases]
+};
+cudaError_t launch_conv_forward(const ConvArgs &, bool bf16, cudaStream_t);
+int conv_backward_blocks(long long ntok);
+cudaError_t launch_conv_backward(const ConvArgs &, bool bf16, float *dweight, float *dbias, cudaStream_t);
+cudaError_t launch_conv_step(const ConvArgs &, bool bf16, cudaStream_t);
+
+constexpr int kSsmCkpt = 128;     // tokens between two recorded states of a sequence
+constexpr int kSsmMaxN = 128;
+
+// Index of sequence n's first recorded state: floor(s0 / 128) + n leaves room for
+// every earlier sequence's ceil(length / 128) records.
+__host__ __device__ inline long long ssm_ckpt_base(long long s0, int n) { return s0 / kSsmCkpt + n; }
+inline long long ssm_ckpt_count(long long ntok, int nseq) { return ntok / kSsmCkpt + nseq + 1; }
+
+struct SsmArgs {
+    SeqAxis ax;
+    int D, G, N;
+    bool softplus;
+    long long ld_x, ld_dt, ld_z, ld_b, ld_c;
+    const void *x, *dt, *Bm, *Cm, *z;
+    const float *A, *Dskip, *dt_bias, *state0;
+    void *out;
+    float *final_state, *states;
+    // backward
+    const void *dout;
+    const float *dfinal;
+    void *dx, *ddt, *dBm, *dCm, *dz;
+    float *dA, *dDskip, *ddt_bias, *dstate0;
+    float *part_bc;    // [tiles][2][N][ntok]
+    float *part_par;   // [nseq][D*N of dA, then D of dDskip, then D of ddt_bias]
+};
+cudaError_t launch_ssm_forward(const SsmArgs &, bool bf16, int sms, cudaStream_t);
+int ssm_backward_tiles(int D, int G);
+cudaError_t launch_ssm_backward(const SsmArgs &, bool bf16, int sms, cudaStream_t);
+cudaError_t launch_ssm_step(const SsmArgs &, bool bf16, cudaStream_t);
+
+constexpr int kNormMaxD = 16384;
+
+struct NormArgs {
+    long long rows;
+    int D;
+    float eps;
+    long long ld_x, ld_res;
+    const void *x, *res;
+    const float *w, *b;
+    void *out, *sum;
+    float *mean, *rstd;
+    // backward
+    const float *cmean, *crstd;
+    const void *dout, *dsum;
+    void *dx;
+    float *part;       // [ctas][2][D]
+};
+cudaError_t launch_norm_forward(const NormArgs &, bool bf16, cudaStream_t);
+int norm_backward_ctas(long long rows, int D, int sms);
+cudaError_t launch_norm_backward(const NormArgs &, bool bf16, int ctas, float *dweight, float *dbias, cudaStream_t);
+
+}  // namespace kla

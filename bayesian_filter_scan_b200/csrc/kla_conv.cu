@@ -1,0 +1,403 @@
+// kla_conv.cu -- short depthwise causal convolution with SiLU: prompts (with a
+// history in and out), gradients, single tokens (sm_100a).
+//   pre[t] = bias + sum_{w<W} weight[w] x[t-(W-1)+w],  out = silu(pre)
+//   d[t] = dout[t] silu'(pre[t]),  dx[t] = sum_{j<W} weight[W-1-j] d[t+j],
+//   dweight[w] = sum_t d[t] x[t-(W-1)+w],  dbias = sum_t d[t]
+// Per channel a few products for 4 to 12 bytes: HBM binds. A thread owns V
+// contiguous channels (one 16-byte access where the rows allow it) and slides
+// along a run of tokens with the last W-1 rows in registers, so every row is
+// read once, but for the W-1 rows in front of each run.
+#include "kla_block.cuh"
+
+namespace kla {
+
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kConvRun = 16;      // tokens of one thread's run, forward
+constexpr int kConvBatch = 8;     // rows in flight per thread
+constexpr int kBwdRun = 32;       // tokens of one thread's run, backward
+constexpr int kBwdRuns = 8;       // runs per CTA
+constexpr int kBwdLanes = 32;     // channel vectors per CTA
+
+// Row `back` places before token t of the sequence that starts at s0: x, or the
+// history's row, or 0.
+template <int W, int V, typename T>
+__device__ __forceinline__ void row_before(const ConvArgs &g, int n, long long s0, long long p, int c, float (&v)[V]) {
+    if (p >= s0) {
+        load_v<V>(static_cast<const T *>(g.x) + p * g.ld_x + c, v);
+    } else if (g.state0) {
+        const long long r = (long long)n * (W - 1) + (W - 1) + (p - s0);
+        load_v<V>(static_cast<const T *>(g.state0) + r * g.D + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+    }
+}
+
+template <int W, int V>
+struct Taps {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const ConvArgs &g, int c) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = __ldg(g.w + (long long)(c + i) * W + k);
+            b[i] = g.bias ? __ldg(g.bias + c + i) : 0.f;
+        }
+    }
+};
+
+// Grid: (token blocks, then one block row per sequence for the final states) x
+// channel blocks; a CTA is bx channel vectors x 128 / bx runs.
+template <int W, int V, typename T>
+__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, long long tok_blocks) {
+    const int cv = blockIdx.y * bx + threadIdx.x % bx, c = cv * V;
+    if (c >= g.D) return;
+    const T *x = static_cast<const T *>(g.x);
+    if (blockIdx.x >= tok_blocks) {
+        // the last W-1 inputs of one sequence
+        if constexpr (W > 1) {
+            const long long n = (blockIdx.x - tok_blocks) * (kConvThreads / bx) + threadIdx.x / bx;
+            if (n >= g.ax.nseq) return;
+            long long s0, s1;
+            g.ax.range((int)n, s0, s1);
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                float v[V];
+                row_before<W, V, T>(g, (int)n, s0, s1 - (W - 1) + i, c, v);
+                store_v<V>(static_cast<T *>(g.final_state) + (n * (W - 1) + i) * g.D + c, v);
+            }
+        }
+        return;
+    }
+    long long t = ((long long)blockIdx.x * (kConvThreads / bx) + threadIdx.x / bx) * kConvRun;
+    const long long te = min(t + kConvRun, g.ax.ntok);
+    if (t >= te) return;
+    Taps<W, V> k;
+    k.load(g, c);
+    float win[W][V];          // rows t-(W-1) .. t
+    int n = -1;
+    long long s0 = 0, s1 = t;  // the current stretch of tokens ends at s1
+    for (; t < te; t += kConvBatch) {
+        float in[kConvBatch][V];
+#pragma unroll
+        for (int j = 0; j < kConvBatch; ++j)
+            if (t + j < te) load_v<V>(x + (t + j) * g.ld_x + c, in[j]);
+#pragma unroll
+        for (int j = 0; j < kConvBatch; ++j) {
+            const long long tj = t + j;
+            if (tj >= te) break;
+            if (tj >= s1) {
+                n = g.ax.find(tj);
+                if (n >= 0) {
+                    g.ax.range(n, s0, s1);
+#pragma unroll
+                    for (int r = 0; r < W - 1; ++r) row_before<W, V, T>(g, n, s0, tj - (W - 1) + r, c, win[r]);
+                } else {
+                    s1 = tj + 1;
+                }
+            }
+            if (n < 0) continue;
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                win[W - 1][i] = in[j][i];
+                float a = k.b[i];
+#pragma unroll
+                for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
+                y[i] = g.silu ? a * sigmoid_f(a) : a;
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r) win[r][i] = win[r + 1][i];
+            }
+            store_v<V>(static_cast<T *>(g.out) + tj * g.D + c, y);
+        }
+    }
+}
+
+// d = dout * silu'(pre) of one token
+template <int W, int V>
+__device__ __forceinline__ void d_pre(const ConvArgs &g, const Taps<W, V> &k, const float (&win)[W][V],
+                                      const float (&dout)[V], float (&d)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        d[i] = dout[i];
+        if (g.silu) {
+            float a = k.b[i];
+#pragma unroll
+            for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
+            const float s = sigmoid_f(a);
+            d[i] *= s * fmaf(a, 1.f - s, 1.f);
+        }
+    }
+}
+
+// A CTA covers 32 channel vectors x 8 runs of 32 tokens. A run slides over its
+// tokens and the W-1 behind them (of the same sequence): dx of a token is
+// complete W-1 tokens later. The runs' sums of dweight and dbias meet in shared
+// memory in run order; the CTAs' sums are added by launch_colsum.
+template <int W, int V, typename T>
+__global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(const ConvArgs g) {
+    __shared__ float red[kBwdRuns][(W + 1) * V][kBwdLanes];
+    const int lane = threadIdx.x % kBwdLanes, run = threadIdx.x / kBwdLanes;
+    const int c = (blockIdx.y * kBwdLanes + lane) * V;
+    const bool live = c < g.D;
+    const T *x = static_cast<const T *>(g.x), *dout = static_cast<const T *>(g.dout);
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) dw[w][i] = 0.f;
+    }
+    const long long a = ((long long)blockIdx.x * kBwdRuns + run) * kBwdRun;
+    const long long b = min(a + kBwdRun, g.ax.ntok);
+    if (live && a < b) {
+        Taps<W, V> k;
+        k.load(g, c);
+        float win[W][V], acc[W][V];   // acc[j]: dx of token t-j so far
+        int n = -1;
+        long long s0 = 0, s1 = a;
+        // dx of token p, complete but for the final state's share
+        auto put = [&](long long p, float (&v)[V]) {
+            if (W > 1 && g.dfinal && p >= s1 - (W - 1)) {
+                float f[V];
+                const long long r = (long long)n * (W - 1) + (W - 1) - (s1 - p);
+                load_v<V>(static_cast<const T *>(g.dfinal) + r * g.D + c, f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] += f[i];
+            }
+            store_v<V>(static_cast<T *>(g.dx) + p * g.D + c, v);
+        };
+        for (long long t = a;; ++t) {
+            if (t >= s1) {
+                if (t >= b) break;
+                n = g.ax.find(t);
+                if (n < 0) {
+                    s1 = t + 1;
+                    continue;
+                }
+                g.ax.range(n, s0, s1);
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r) {
+                    row_before<W, V, T>(g, n, s0, t - (W - 1) + r, c, win[r]);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[r][i] = 0.f;
+                }
+            }
+            float o[V], d[V];
+            load_v<V>(x + t * g.ld_x + c, win[W - 1]);
+            load_v<V>(dout + t * g.D + c, o);
+            d_pre<W, V>(g, k, win, o, d);
+#pragma unroll
+            for (int j = W - 1; j > 0; --j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[j][i] = fmaf(k.w[W - 1 - j][i], d[i], acc[j - 1][i]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[0][i] = k.w[W - 1][i] * d[i];
+            if (t < b) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[i];
+#pragma unroll
+                    for (int w = 0; w < W; ++w) dw[w][i] = fmaf(d[i], win[w][i], dw[w][i]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < W - 1; ++r)
+#pragma unroll
+                for (int i = 0; i < V; ++i) win[r][i] = win[r + 1][i];
+            // token t-(W-1) is complete; at the sequence's end (or the halo's) so are the ones behind it
+            const long long lo = max(a, s0);
+            if (t - (W - 1) >= lo) put(t - (W - 1), acc[W - 1]);
+            if (t + 1 == s1) {
+#pragma unroll
+                for (int j = W - 2; j >= 0; --j)
+                    if (t - j >= lo && t - j < b) put(t - j, acc[j]);
+            }
+            if (t + 1 >= b + (W - 1)) break;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) red[run][w * V + i][lane] = dw[w][i];
+        red[run][W * V + i][lane] = db[i];
+    }
+    __syncthreads();
+    float *part = g.part + (long long)blockIdx.x * g.D * (W + 1);
+    for (int e = threadIdx.x; e < (W + 1) * V * kBwdLanes; e += kBwdLanes * kBwdRuns) {
+        const int l = e % kBwdLanes, q = e / kBwdLanes, w = q / V, i = q % V;
+        const int ch = (blockIdx.y * kBwdLanes + l) * V + i;
+        if (ch >= g.D) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < kBwdRuns; ++r) s += red[r][q][l];
+        part[w < W ? (long long)ch * W + w : (long long)g.D * W + ch] = s;
+    }
+}
+
+// dstate0[n][i] = sum over tokens p <= i of weight[i-p] d[p], plus what of the
+// final state was the history itself (sequences shorter than W-1).
+template <int W, typename T>
+__global__ void __launch_bounds__(kConvThreads) conv_dstate_kernel(const ConvArgs g) {
+    if constexpr (W > 1) {
+        const int c = blockIdx.y * kConvThreads + threadIdx.x;
+        if (c >= g.D) return;
+        const int n = blockIdx.x;
+        long long s0, s1;
+        g.ax.range(n, s0, s1);
+        const long long len = s1 - s0;
+        Taps<W, 1> k;
+        k.load(g, c);
+        float ds[W - 1], win[W][1];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const long long from = i - len;     // final_state[i - len] was state0[i]
+            ds[i] = g.dfinal && from >= 0
+                        ? to_f(static_cast<const T *>(g.dfinal)[((long long)n * (W - 1) + from) * g.D + c]) : 0.f;
+            row_before<W, 1, T>(g, n, s0, s0 - (W - 1) + i, c, win[i]);
+        }
+#pragma unroll
+        for (int p = 0; p < W - 1; ++p) {
+            if (p < len) {
+                float o[1], d[1];
+                load_v<1>(static_cast<const T *>(g.x) + (s0 + p) * g.ld_x + c, win[W - 1]);
+                load_v<1>(static_cast<const T *>(g.dout) + (s0 + p) * g.D + c, o);
+                d_pre<W, 1>(g, k, win, o, d);
+#pragma unroll
+                for (int i = p; i < W - 1; ++i) ds[i] = fmaf(k.w[i - p][0], d[0], ds[i]);
+#pragma unroll
+                for (int r = 0; r < W - 1; ++r) win[r][0] = win[r + 1][0];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+            static_cast<T *>(g.dstate0)[((long long)n * (W - 1) + i) * g.D + c] = from_f<T>(ds[i]);
+    }
+}
+
+// One token per row: the state's rows move down by one, x becomes the last.
+template <int W, int V, typename T>
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvArgs g, int nvec) {
+    const long long e = (long long)blockIdx.x * kConvThreads + threadIdx.x;
+    const long long n = e / nvec;
+    if (n >= g.ax.nseq) return;
+    const int c = (int)(e - n * nvec) * V;
+    T *state = static_cast<T *>(g.final_state) + n * (W - 1) * g.D + c;
+    float win[W][V], y[V];
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) load_v<V>(state + (long long)r * g.D, win[r]);
+    load_v<V>(static_cast<const T *>(g.x) + n * g.ld_x + c, win[W - 1]);
+    Taps<W, V> k;
+    k.load(g, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float a = k.b[i];
+#pragma unroll
+        for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
+        y[i] = g.silu ? a * sigmoid_f(a) : a;
+    }
+    store_v<V>(static_cast<T *>(g.out) + n * g.D + c, y);
+#pragma unroll
+    for (int r = 0; r < W - 1; ++r) store_v<V>(state + (long long)r * g.D, win[r + 1]);
+}
+
+bool al(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Whether every row of the call's tensors starts on an `a`-byte boundary.
+bool rows_aligned(const ConvArgs &g, int es, size_t a) {
+    for (const void *p : {g.x, g.state0, (const void *)g.out, (const void *)g.final_state, g.dout, g.dfinal,
+                          (const void *)g.dx, (const void *)g.dstate0})
+        if (!al(p, a)) return false;
+    return ((size_t)g.D * es) % a == 0 && ((size_t)g.ld_x * es) % a == 0;
+}
+
+template <int W, int V, typename T>
+cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
+    const int nvec = (g.D + V - 1) / V;
+    int bx = 1;
+    while (bx < nvec && bx < kConvThreads) bx *= 2;
+    const int runs = kConvThreads / bx;
+    const long long tok_blocks = (g.ax.ntok + (long long)runs * kConvRun - 1) / ((long long)runs * kConvRun);
+    const long long seq_blocks = (W > 1 && g.final_state) ? (g.ax.nseq + runs - 1) / runs : 0;
+    if (tok_blocks + seq_blocks == 0) return cudaSuccess;
+    if (tok_blocks + seq_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(tok_blocks + seq_blocks), (unsigned)((nvec + bx - 1) / bx));
+    conv_forward_kernel<W, V, T><<<grid, kConvThreads, 0, st>>>(g, bx, tok_blocks);
+    return cudaGetLastError();
+}
+
+template <int W, int V, typename T>
+cudaError_t backward_t(const ConvArgs &g, cudaStream_t st) {
+    const int nvec = (g.D + V - 1) / V;
+    const int blocks = conv_backward_blocks(g.ax.ntok);
+    if (blocks) {
+        const dim3 grid((unsigned)blocks, (unsigned)((nvec + kBwdLanes - 1) / kBwdLanes));
+        conv_backward_kernel<W, V, T><<<grid, kBwdLanes * kBwdRuns, 0, st>>>(g);
+    }
+    if (W > 1 && g.dstate0 && g.ax.nseq) {
+        const dim3 grid((unsigned)g.ax.nseq, (unsigned)((g.D + kConvThreads - 1) / kConvThreads));
+        conv_dstate_kernel<W, T><<<grid, kConvThreads, 0, st>>>(g);
+    }
+    return cudaGetLastError();
+}
+
+template <int W, int V, typename T>
+cudaError_t step_t(const ConvArgs &g, cudaStream_t st) {
+    const int nvec = (g.D + V - 1) / V;
+    const long long n = (long long)nvec * g.ax.nseq, blocks = (n + kConvThreads - 1) / kConvThreads;
+    if (!blocks) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    conv_step_kernel<W, V, T><<<(unsigned)blocks, kConvThreads, 0, st>>>(g, nvec);
+    return cudaGetLastError();
+}
+
+enum class Call { kForward, kBackward, kStep };
+
+template <int W, typename T>
+cudaError_t conv_w(const ConvArgs &g, Call call, cudaStream_t st) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool vec = rows_aligned(g, sizeof(T), call == Call::kBackward ? 8 : 16);
+    if (call == Call::kForward) return vec ? forward_t<W, V, T>(g, st) : forward_t<W, 1, T>(g, st);
+    if (call == Call::kStep) return vec ? step_t<W, V, T>(g, st) : step_t<W, 1, T>(g, st);
+    // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers
+    return vec ? backward_t<W, V / 2, T>(g, st) : backward_t<W, 1, T>(g, st);
+}
+
+template <typename T>
+cudaError_t conv_t(const ConvArgs &g, Call call, cudaStream_t st) {
+    switch (g.W) {
+        case 1: return conv_w<1, T>(g, call, st);
+        case 2: return conv_w<2, T>(g, call, st);
+        case 3: return conv_w<3, T>(g, call, st);
+        default: return conv_w<4, T>(g, call, st);
+    }
+}
+
+cudaError_t conv_any(const ConvArgs &g, bool bf16, Call call, cudaStream_t st) {
+    return bf16 ? conv_t<__nv_bfloat16>(g, call, st) : conv_t<float>(g, call, st);
+}
+
+}  // namespace
+
+cudaError_t launch_conv_forward(const ConvArgs &g, bool bf16, cudaStream_t st) {
+    return conv_any(g, bf16, Call::kForward, st);
+}
+
+int conv_backward_blocks(long long ntok) {
+    return (int)((ntok + kBwdRuns * kBwdRun - 1) / (kBwdRuns * kBwdRun));
+}
+
+cudaError_t launch_conv_backward(const ConvArgs &g, bool bf16, float *dweight, float *dbias, cudaStream_t st) {
+    cudaError_t e = conv_any(g, bf16, Call::kBackward, st);
+    if (e != cudaSuccess) return e;
+    return launch_colsum(g.part, conv_backward_blocks(g.ax.ntok), (long long)g.D * (g.W + 1), (long long)g.D * g.W,
+                         dweight, g.D, dbias, nullptr, st);
+}
+
+cudaError_t launch_conv_step(const ConvArgs &g, bool bf16, cudaStream_t st) {
+    return conv_any(g, bf16, Call::kStep, st);
+}
+
+}  // namespace kla

@@ -28,7 +28,13 @@ EXPORTS = ("kla_workspace_bytes", "kla_precision_workspace_bytes", "kla_forward"
            "kla_plan", "kla_precision",
            "kla_decode_step", "kla_host_device_bytes", "kla_forward_host", "kla_check",
            "kla_status_string", "kla_version", "kla_forward_noalloc", "kla_kdn_forward",
-           "kla_prologue", "kla_backward_workspace_bytes", "kla_backward")
+           "kla_prologue", "kla_backward_workspace_bytes", "kla_backward",
+           "kla_conv_forward", "kla_conv_backward_workspace_bytes", "kla_conv_backward", "kla_conv_step",
+           "kla_ssm_states_bytes", "kla_ssm_forward", "kla_ssm_backward_workspace_bytes", "kla_ssm_backward",
+           "kla_ssm_step", "kla_layernorm_forward", "kla_layernorm_backward_workspace_bytes",
+           "kla_layernorm_backward")
+# Tokens between two recorded states, and the most states per channel (include/kla.h kla_ssm_forward)
+SSM_STATE_EVERY, SSM_MAX_STATES = 128, 128
 
 
 class KlaError(RuntimeError):
@@ -41,6 +47,25 @@ class KlaDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("mode", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int)]
+
+
+class KlaConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("W", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("silu", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+                ("num_seqs", ctypes.c_int), ("ld_x", ctypes.c_longlong)]
+
+
+class KlaSsmDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("G", ctypes.c_int),
+                ("N", ctypes.c_int), ("dtype", ctypes.c_int), ("softplus", ctypes.c_int),
+                ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int), ("ld_x", ctypes.c_longlong),
+                ("ld_dt", ctypes.c_longlong), ("ld_z", ctypes.c_longlong), ("ld_b", ctypes.c_longlong),
+                ("ld_c", ctypes.c_longlong)]
+
+
+class KlaNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("ld_x", ctypes.c_longlong), ("ld_residual", ctypes.c_longlong)]
 
 
 _lib = None
@@ -85,6 +110,22 @@ def lib():
         L.kla_backward_workspace_bytes.restype = ctypes.c_size_t
         L.kla_backward.argtypes = [D] + [_P] * 19 + [_P, ctypes.c_size_t, _P]
         L.kla_backward.restype = ctypes.c_int
+        S, CD, SD, ND = ctypes.c_size_t, *(ctypes.POINTER(t) for t in (KlaConvDesc, KlaSsmDesc, KlaNormDesc))
+        for name, res, args in (
+                ("kla_conv_forward", ctypes.c_int, [CD] + [_P] * 7),
+                ("kla_conv_backward_workspace_bytes", S, [CD]),
+                ("kla_conv_backward", ctypes.c_int, [CD] + [_P] * 11 + [S, _P]),
+                ("kla_conv_step", ctypes.c_int, [CD] + [_P] * 6),
+                ("kla_ssm_states_bytes", S, [SD]),
+                ("kla_ssm_forward", ctypes.c_int, [SD] + [_P] * 13),
+                ("kla_ssm_backward_workspace_bytes", S, [SD, ctypes.c_int]),
+                ("kla_ssm_backward", ctypes.c_int, [SD] + [_P] * 22 + [S, _P]),
+                ("kla_ssm_step", ctypes.c_int, [SD] + [_P] * 11),
+                ("kla_layernorm_forward", ctypes.c_int, [ND] + [_P] * 9),
+                ("kla_layernorm_backward_workspace_bytes", S, [ND]),
+                ("kla_layernorm_backward", ctypes.c_int, [ND] + [_P] * 10 + [S, _P])):
+            f = getattr(L, name)
+            f.restype, f.argtypes = res, args
         L.kla_check.argtypes = [_P]
         L.kla_check.restype = ctypes.c_int
         L.kla_status_string.argtypes = [ctypes.c_int]
@@ -332,6 +373,314 @@ def forward_noalloc(q, k, v, a, qn, beta, lambda0=None, eta0=None, B=None, T=Non
                                   _ptr(lambda0), _ptr(eta0), _ptr(out), _ptr(fl), _ptr(fe), _stream())
     _check(s, "kla_forward_noalloc")
     return (out, fl, fe) if final_state else out
+
+
+# ---- the recurrent block around the mixers: short convolution, selective scan, layer norm ----
+
+_F32, _DTYPES = torch.float32, {torch.bfloat16: KLA_BF16, torch.float32: KLA_FP32}
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """The device of a call's tensors made current while the call enqueues its
+    work; the work goes on that device's current stream."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device):
+        self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _io_dtype(x):
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if x.dtype not in _DTYPES:
+        raise TypeError("token tensors must be bfloat16 or float32")
+    return _DTYPES[x.dtype]
+
+
+def _tokens(name, t, like, shape):
+    """A token tensor: like's dtype and device, the given shape, rows at one
+    stride with contiguous values. Returns the token stride."""
+    if t.dtype != like.dtype:
+        raise TypeError("%s must have the dtype of x" % name)
+    if t.device != like.device:
+        raise ValueError("%s must be on the device of x" % name)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
+    width = 1
+    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and st != width:
+            raise ValueError("the values of a row of %s must be contiguous" % name)
+        width *= n
+    if shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError("rows of %s must not overlap" % name)
+    return t.stride(0)
+
+
+def _dense(name, t, like, shape, dtype=_F32):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
+    if t.device != like.device:
+        raise ValueError("%s must be on the device of x" % name)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape %s" % (name, shape))
+
+
+def _axis(x, cu_seqlens, B, T):
+    """(rows, tokens per row, offsets pointer, packed sequences, sequences) of the token axis of x."""
+    n = x.shape[0]
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device:
+            raise TypeError("cu_seqlens must be an int32 tensor on the device of x")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2 or not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be contiguous with at least two offsets")
+        if B is not None or T is not None:
+            raise ValueError("B and T do not go with cu_seqlens")
+        k = cu_seqlens.numel() - 1
+        return 1, n, cu_seqlens.data_ptr(), k, k
+    if B is None:
+        B = 1 if T is None else (n // T if T else 0)
+    T = T if T is not None else (n // B if B else 0)
+    if B < 0 or T < 0 or B * T != n:
+        raise ValueError("B*T must equal the number of tokens")
+    return B, T, None, 0, B
+
+
+def _out_like(name, out, x, shape):
+    if out is None:
+        return torch.empty(shape, dtype=x.dtype, device=x.device)
+    _dense(name, out, x, shape, x.dtype)
+    return out
+
+
+def _conv(x, weight, bias, cu_seqlens, B, T, silu):
+    dt = _io_dtype(x)
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be [Ntok, D] and weight [D, W]")
+    D, W = x.shape[1], weight.shape[1]
+    if not 1 <= W <= 4:
+        raise ValueError("a convolution has 1 to 4 taps")
+    ld = _tokens("x", x, x, tuple(x.shape))
+    _dense("weight", weight, x, (D, W))
+    _dense("bias", bias, x, (D,))
+    b, t, cu, k, N = _axis(x, cu_seqlens, B, T)
+    return KlaConvDesc(b, t, D, W, dt, 1 if silu else 0, cu, k, ld), D, W, N
+
+
+def conv_forward(x, weight, bias=None, state0=None, cu_seqlens=None, B=None, T=None, silu=True, final_state=False,
+                 out=None):
+    """Short causal convolution with SiLU (include/kla.h kla_conv_forward): x
+    [Ntok, D] (rows may be strided), weight [D, W], bias [D]; the history state0
+    [N, W-1, D] holds the inputs before each sequence. Returns ``out`` or
+    ``(out, state)`` with ``final_state``: the history after each sequence."""
+    d, D, W, N = _conv(x, weight, bias, cu_seqlens, B, T, silu)
+    _dense("state0", state0, x, (N, W - 1, D), x.dtype)
+    with _on(x.device) as stream:
+        out = _out_like("out", out, x, (x.shape[0], D))
+        fs = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device) if final_state else None
+        s = lib().kla_conv_forward(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(out), _p(fs), stream)
+    _check(s, "kla_conv_forward")
+    return (out, fs) if final_state else out
+
+
+def conv_backward(x, weight, dout, bias=None, state0=None, dfinal_state=None, cu_seqlens=None, B=None, T=None,
+                  silu=True, workspace=None):
+    """Gradients of ``conv_forward`` (include/kla.h kla_conv_backward): a dict of
+    ``dx`` and ``dstate0`` (x's dtype; dstate0 only with a state0) and ``dweight``,
+    ``dbias`` (fp32)."""
+    d, D, W, N = _conv(x, weight, bias, cu_seqlens, B, T, silu)
+    _dense("dout", dout, x, (x.shape[0], D), x.dtype)
+    _dense("state0", state0, x, (N, W - 1, D), x.dtype)
+    _dense("dfinal_state", dfinal_state, x, (N, W - 1, D), x.dtype)
+    with _on(x.device) as stream:
+        io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
+        g = {"dx": torch.empty((x.shape[0], D), **io), "dweight": torch.empty((D, W), **f32),
+             "dbias": torch.empty(D, **f32)}
+        if state0 is not None:
+            g["dstate0"] = torch.empty((N, W - 1, D), **io)
+        need = lib().kla_conv_backward_workspace_bytes(ctypes.byref(d))
+        workspace = _workspace(workspace, need, x)
+        s = lib().kla_conv_backward(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(dout),
+                                    _p(dfinal_state), _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]),
+                                    _p(g.get("dstate0")), _p(workspace), workspace.numel(), stream)
+    _check(s, "kla_conv_backward")
+    return g
+
+
+def _workspace(ws, need, x):
+    if ws is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+    if ws.dtype != torch.uint8 or ws.device != x.device or not ws.is_contiguous() or ws.numel() < need:
+        raise ValueError("workspace must be a contiguous uint8 tensor of at least %d bytes on the device of x" % need)
+    return ws
+
+
+def conv_step(x, weight, state, bias=None, silu=True, out=None):
+    """One token per row: x [B, D]; ``state`` [B, W-1, D] is shifted in place.
+    Returns out [B, D]."""
+    d, D, W, N = _conv(x, weight, bias, None, x.shape[0], 1, silu)
+    _dense("state", state, x, (N, W - 1, D), x.dtype)
+    with _on(x.device) as stream:
+        out = _out_like("out", out, x, (N, D))
+        s = lib().kla_conv_step(ctypes.byref(d), x.data_ptr(), weight.data_ptr(), _p(bias), _p(state),
+                                out.data_ptr(), stream)
+    _check(s, "kla_conv_step")
+    return out
+
+
+def _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus):
+    io = _io_dtype(x)
+    if x.dim() != 2 or A.dim() != 2 or Bm.dim() != 3:
+        raise ValueError("x must be [Ntok, D], A [D, N], Bm and Cm [Ntok, G, N]")
+    n, ch = x.shape
+    G, N = Bm.shape[1], A.shape[1]
+    if G < 1 or ch % G:
+        raise ValueError("the groups of Bm must divide the channels")
+    ld = (_tokens("x", x, x, (n, ch)), _tokens("dt", dt, x, (n, ch)),
+          _tokens("z", z, x, (n, ch)) if z is not None else 0,
+          _tokens("Bm", Bm, x, (n, G, N)), _tokens("Cm", Cm, x, (n, G, N)))
+    _dense("A", A, x, (ch, N))
+    _dense("D", D, x, (ch,))
+    _dense("dt_bias", dt_bias, x, (ch,))
+    b, t, cu, k, seqs = _axis(x, cu_seqlens, B, T)
+    return KlaSsmDesc(b, t, ch, G, N, io, 1 if softplus else 0, cu, k, *ld), ch, N, G, seqs
+
+
+def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state0=None, cu_seqlens=None, B=None, T=None,
+                softplus=True, final_state=False, save_states=False, out=None):
+    """Selective state space scan (include/kla.h kla_ssm_forward): x, dt, z
+    [Ntok, D], Bm, Cm [Ntok, G, N] (rows may be strided), A [D, N], D and dt_bias
+    [D], state0 [Nseq, D, N]. Returns ``out``, then the final state with
+    ``final_state``, then what ``ssm_backward`` takes as ``states`` with
+    ``save_states``."""
+    d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
+    _dense("state0", state0, x, (seqs, ch, N))
+    with _on(x.device) as stream:
+        out = _out_like("out", out, x, (x.shape[0], ch))
+        fs = torch.empty((seqs, ch, N), dtype=_F32, device=x.device) if final_state else None
+        st = None
+        if save_states:
+            st = torch.empty(lib().kla_ssm_states_bytes(ctypes.byref(d)) // 4, dtype=_F32, device=x.device)
+        s = lib().kla_ssm_forward(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
+                                  _p(state0), _p(out), _p(fs), _p(st), stream)
+    _check(s, "kla_ssm_forward")
+    res = (out,) + ((fs,) if final_state else ()) + ((st,) if save_states else ())
+    return res if len(res) > 1 else out
+
+
+def ssm_backward(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, state0=None, dfinal_state=None, states=None,
+                 cu_seqlens=None, B=None, T=None, softplus=True, workspace=None):
+    """Gradients of ``ssm_forward`` (include/kla.h kla_ssm_backward): a dict of
+    ``dx, ddt, dBm, dCm`` and ``dz`` (with z) in x's dtype, and ``dA, dD,
+    ddt_bias, dstate0`` in fp32. ``states``: what the forward call returned with
+    ``save_states`` for the same inputs (walked again without)."""
+    d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
+    n = x.shape[0]
+    _dense("dout", dout, x, (n, ch), x.dtype)
+    _dense("state0", state0, x, (seqs, ch, N))
+    _dense("dfinal_state", dfinal_state, x, (seqs, ch, N))
+    L = lib()
+    if states is not None:
+        _dense("states", states, x, (L.kla_ssm_states_bytes(ctypes.byref(d)) // 4,))
+    with _on(x.device) as stream:
+        io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
+        g = {"dx": torch.empty((n, ch), **io), "ddt": torch.empty((n, ch), **io),
+             "dBm": torch.empty((n, G, N), **io), "dCm": torch.empty((n, G, N), **io),
+             "dA": torch.empty((ch, N), **f32), "dD": torch.empty(ch, **f32), "ddt_bias": torch.empty(ch, **f32),
+             "dstate0": torch.empty((seqs, ch, N), **f32)}
+        if z is not None:
+            g["dz"] = torch.empty((n, ch), **io)
+        workspace = _workspace(workspace, L.kla_ssm_backward_workspace_bytes(ctypes.byref(d), states is not None), x)
+        s = L.kla_ssm_backward(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
+                               _p(state0), _p(states), _p(dout), _p(dfinal_state), _p(g["dx"]), _p(g["ddt"]),
+                               _p(g["dA"]), _p(g["dBm"]), _p(g["dCm"]), _p(g["dD"]), _p(g.get("dz")),
+                               _p(g["ddt_bias"]), _p(g["dstate0"]), _p(workspace), workspace.numel(), stream)
+    _check(s, "kla_ssm_backward")
+    return g
+
+
+def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, softplus=True, out=None):
+    """One token per row through the scan: x, dt, z [B, D], Bm, Cm [B, G, N];
+    ``state`` [B, D, N] is updated in place. Returns out [B, D]."""
+    d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, None, x.shape[0], 1, softplus)
+    _dense("state", state, x, (seqs, ch, N))
+    with _on(x.device) as stream:
+        out = _out_like("out", out, x, (seqs, ch))
+        s = lib().kla_ssm_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                               Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), state.data_ptr(), out.data_ptr(), stream)
+    _check(s, "kla_ssm_step")
+    return out
+
+
+def _norm(x, weight, bias, residual, eps):
+    dt = _io_dtype(x)
+    if x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError("x must be [rows, D]")
+    shape = tuple(x.shape)
+    ld = _tokens("x", x, x, shape)
+    ld_r = _tokens("residual", residual, x, shape) if residual is not None else 0
+    _dense("weight", weight, x, shape[1:])
+    _dense("bias", bias, x, shape[1:])
+    return KlaNormDesc(shape[0], shape[1], dt, eps, ld, ld_r), shape
+
+
+def layernorm_forward(x, weight=None, bias=None, residual=None, eps=1e-5, stats=False, out=None, sum_out=None):
+    """Layer norm over the last axis of x [rows, D], or of x + residual
+    (include/kla.h kla_layernorm_forward). Returns ``out``, then the sum with a
+    residual, then ``mean, rstd`` with ``stats``."""
+    d, shape = _norm(x, weight, bias, residual, eps)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out goes with a residual")
+    with _on(x.device) as stream:
+        out = _out_like("out", out, x, shape)
+        total = _out_like("sum_out", sum_out, x, shape) if residual is not None else None
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(shape[0], dtype=_F32, device=x.device)
+            rstd = torch.empty(shape[0], dtype=_F32, device=x.device)
+        s = lib().kla_layernorm_forward(ctypes.byref(d), _p(x), _p(residual), _p(weight), _p(bias), _p(out),
+                                        _p(total), _p(mean), _p(rstd), stream)
+    _check(s, "kla_layernorm_forward")
+    res = (out,) + ((total,) if residual is not None else ()) + ((mean, rstd) if stats else ())
+    return res if len(res) > 1 else out
+
+
+def layernorm_backward(x, dout, mean, rstd, weight=None, dsum=None, workspace=None):
+    """Gradients of ``layernorm_forward`` (include/kla.h kla_layernorm_backward): x
+    is the tensor that was normalised (the sum, with a residual) and dsum the
+    gradient that reaches it past the norm. A dict of ``dx`` (x's dtype; of the
+    residual alike) and ``dweight``, ``dbias`` (fp32)."""
+    d, shape = _norm(x, weight, None, None, 1.0)
+    _dense("mean", mean, x, shape[:1])
+    _dense("rstd", rstd, x, shape[:1])
+    _dense("dout", dout, x, shape, x.dtype)
+    _dense("dsum", dsum, x, shape, x.dtype)
+    with _on(x.device) as stream:
+        f32 = dict(dtype=_F32, device=x.device)
+        g = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device), "dweight": torch.empty(shape[1], **f32),
+             "dbias": torch.empty(shape[1], **f32)}
+        workspace = _workspace(workspace, lib().kla_layernorm_backward_workspace_bytes(ctypes.byref(d)), x)
+        s = lib().kla_layernorm_backward(ctypes.byref(d), _p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dsum),
+                                         _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]), _p(workspace),
+                                         workspace.numel(), stream)
+    _check(s, "kla_layernorm_backward")
+    return g
 
 
 def check(stream=None):

@@ -285,6 +285,148 @@ kla_status kla_backward(const kla_desc *desc,
                         float *dlambda0, float *deta0,
                         void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- the recurrent block around the mixers ------------------------------------
+ *
+ * Short causal convolution, selective state space scan and layer norm. These
+ * take plain token tensors: tokens of all sequences on one axis (Ntok = B*T),
+ * channels contiguous. "ld" strides are the distance between two tokens' rows
+ * in elements, so a tensor may be a column slice of a wider projection; 0 stands
+ * for a contiguous tensor. Sequences are B rows of T tokens, or num_seqs packed
+ * sequences with cu_seqlens as in kla_desc (a sequence may be empty; tokens
+ * before the first offset or behind the last one belong to none: their output
+ * rows are left as they were and they enter no sum). Pointers need the alignment of
+ * their element type only; 16-byte aligned rows move as vectors. Outputs may
+ * not overlap inputs or each other (checked; KLA_ERR_INVALID_ARG), except where
+ * a call updates a state in place. With no tokens at all, states pass through
+ * and gradients of parameters are zero. All reductions have a fixed order:
+ * identical inputs give bitwise identical outputs.
+ */
+
+typedef struct {
+    int B, T, D;            /* rows, tokens per row, channels */
+    int W;                  /* taps, 1..4 */
+    kla_dtype dtype;        /* x, out, states and their gradients */
+    int silu;               /* nonzero: out = silu(conv), else out = conv */
+    const int *cu_seqlens;
+    int num_seqs;
+    long long ld_x;         /* token stride of x */
+} kla_conv_desc;
+
+/* Depthwise causal convolution with SiLU (Kalman Linear Attention, technical
+ * summary section 4: a Mamba-like block with a 1-D causal convolution), with
+ * the history that the prologue's convolution lacks:
+ *   out[t,c] = act(bias[c] + sum_{w<W} weight[c,w] x[t-(W-1)+w, c]),
+ * where places before a sequence's start are read from state0 [N, W-1, D] (its
+ * last row is the token just before the sequence), or are 0 when state0 is NULL.
+ * final_state [N, W-1, D] (or NULL) receives the last W-1 inputs, so that two
+ * calls over a split sequence equal one over the whole. weight [D, W], bias [D]
+ * (or NULL) fp32. out [Ntok, D] contiguous. With W = 1 the states are empty and
+ * their pointers are ignored. */
+kla_status kla_conv_forward(const kla_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                            const void *state0, void *out, void *final_state, cudaStream_t stream);
+
+/* Gradients of kla_conv_forward, given dout [Ntok, D] (contiguous, desc->dtype)
+ * and dfinal_state (or NULL for zero): dx [Ntok, D] contiguous and dstate0
+ * [N, W-1, D] (or NULL) in desc->dtype, dweight [D, W] and dbias [D] (or NULL) in
+ * fp32. The pre-activation is recomputed. workspace: 16-byte aligned,
+ * kla_conv_backward_workspace_bytes. */
+size_t kla_conv_backward_workspace_bytes(const kla_conv_desc *desc);
+kla_status kla_conv_backward(const kla_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                             const void *state0, const void *dout, const void *dfinal_state,
+                             void *dx, float *dweight, float *dbias, void *dstate0,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One token per sequence (desc->T must be 1, cu_seqlens NULL): x [B, D], out
+ * [B, D], state [B, W-1, D] holds the last W-1 inputs and is shifted in place. */
+kla_status kla_conv_step(const kla_conv_desc *desc, const void *x, const float *weight, const float *bias,
+                         void *state, void *out, cudaStream_t stream);
+
+typedef struct {
+    int B, T;               /* rows, tokens per row */
+    int D, G;               /* channels, and groups that share B and C; G divides D */
+    int N;                  /* states per channel, 1..128 */
+    kla_dtype dtype;        /* x, dt, z, Bm, Cm, out and their gradients */
+    int softplus;           /* nonzero: delta = softplus(dt + dt_bias), else dt + dt_bias */
+    const int *cu_seqlens;
+    int num_seqs;
+    long long ld_x, ld_dt, ld_z, ld_b, ld_c;  /* token strides of x, dt, z, Bm, Cm */
+} kla_ssm_desc;
+
+/* Selective state space scan: a diagonal linear recurrence whose step delta and
+ * projections depend on the token, the mixer that Mamba-like blocks put where
+ * kla_forward stands. Per channel d (of group g(d) = d / (D/G)) and state n:
+ *   delta = softplus(dt[t,d] + dt_bias[d])
+ *   h[d,n] <- exp(delta A[d,n]) h[d,n] + delta x[t,d] Bm[t,g,n]
+ *   out[t,d] = (sum_n Cm[t,g,n] h[d,n] + Dskip[d] x[t,d]) * silu(z[t,d])
+ * x, dt, z [Ntok, D]; Bm, Cm [Ntok, G, N]; A [D, N], Dskip [D], dt_bias [D] and
+ * state0, final_state [Nseq, D, N] fp32; out [Ntok, D] contiguous. z, Dskip,
+ * dt_bias, state0 (0), final_state may be NULL. The state is held in fp32.
+ * states (or NULL): kla_ssm_states_bytes bytes, 16-byte aligned, receive the
+ * state before every 128th token of each sequence for kla_ssm_backward.
+ * Preconditions not checked on the device: finite inputs, delta*A <= 0 for a
+ * recurrence that stays bounded. N > 128 returns KLA_ERR_UNSUPPORTED. */
+size_t kla_ssm_states_bytes(const kla_ssm_desc *desc);
+kla_status kla_ssm_forward(const kla_ssm_desc *desc, const void *x, const void *dt, const float *A,
+                           const void *Bm, const void *Cm, const float *Dskip, const void *z,
+                           const float *dt_bias, const float *state0, void *out, float *final_state,
+                           float *states, cudaStream_t stream);
+
+/* Gradients of kla_ssm_forward, given dout [Ntok, D] (contiguous, desc->dtype)
+ * and dfinal_state (or NULL for zero): dx, ddt, dz [Ntok, D], dBm, dCm
+ * [Ntok, G, N] contiguous in desc->dtype (the type the projections' products
+ * read them in; every sum is fp32 and rounded once); dA [D, N], dDskip [D],
+ * ddt_bias [D] and dstate0 [Nseq, D, N] in fp32. dDskip, ddt_bias and dstate0
+ * may be NULL; dz goes with z (both or neither). states: what the forward call
+ * recorded for the same inputs, or NULL to have the states walked again.
+ * workspace: 16-byte aligned, kla_ssm_backward_workspace_bytes(desc, states
+ * given or not). */
+size_t kla_ssm_backward_workspace_bytes(const kla_ssm_desc *desc, int with_states);
+kla_status kla_ssm_backward(const kla_ssm_desc *desc, const void *x, const void *dt, const float *A,
+                            const void *Bm, const void *Cm, const float *Dskip, const void *z,
+                            const float *dt_bias, const float *state0, const float *states,
+                            const void *dout, const float *dfinal_state,
+                            void *dx, void *ddt, float *dA, void *dBm, void *dCm, float *dDskip, void *dz,
+                            float *ddt_bias, float *dstate0,
+                            void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One token per sequence (desc->T must be 1, cu_seqlens NULL): as
+ * kla_ssm_forward with state [B, D, N] updated in place. */
+kla_status kla_ssm_step(const kla_ssm_desc *desc, const void *x, const void *dt, const float *A,
+                        const void *Bm, const void *Cm, const float *Dskip, const void *z,
+                        const float *dt_bias, float *state, void *out, cudaStream_t stream);
+
+typedef struct {
+    long long rows;
+    int D;                  /* values per row, 1..16384 */
+    kla_dtype dtype;        /* x, residual, out, sum and their gradients */
+    float eps;              /* > 0 */
+    long long ld_x, ld_residual;  /* row strides of x and residual */
+} kla_norm_desc;
+
+/* Layer norm over the last axis, of x or of the residual sum x + residual (the
+ * norm in front of a block, or of every head's output with rows = Ntok*H):
+ *   s = x + residual (rounded to dtype), out = (s - mean) * rstd * weight + bias,
+ *   rstd = 1/sqrt(mean((s - mean)^2) + eps).
+ * weight, bias [D] fp32 or NULL for 1 and 0. residual NULL: s = x. out [rows, D]
+ * contiguous; sum [rows, D] (goes with residual, or NULL) receives s; mean, rstd
+ * [rows] fp32 or NULL. sum may be the residual's or x's own buffer, and out x's,
+ * when that tensor is contiguous. */
+kla_status kla_layernorm_forward(const kla_norm_desc *desc, const void *x, const void *residual,
+                                 const float *weight, const float *bias, void *out, void *sum,
+                                 float *mean, float *rstd, cudaStream_t stream);
+
+/* Gradients of kla_layernorm_forward: x is the tensor that was normalised (s,
+ * with a residual; ld_x its stride), mean and rstd what the forward call wrote,
+ * dout [rows, D] contiguous, dsum [rows, D] contiguous or NULL the gradient that
+ * reaches s past the norm. dx [rows, D] in dtype (the gradient of x and of the
+ * residual alike, dsum included), dweight and dbias [D] fp32 or NULL. workspace:
+ * 16-byte aligned, kla_layernorm_backward_workspace_bytes. */
+size_t kla_layernorm_backward_workspace_bytes(const kla_norm_desc *desc);
+kla_status kla_layernorm_backward(const kla_norm_desc *desc, const void *x, const float *weight,
+                                  const float *mean, const float *rstd, const void *dout, const void *dsum,
+                                  void *dx, float *dweight, float *dbias,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the library's device status
  * word on the current device: KLA_OK, KLA_ERR_RANGE or KLA_ERR_TIMEOUT from any
  * kernel that ran since the last check, or KLA_ERR_CUDA if the stream failed.
