@@ -65,7 +65,7 @@ cudaError_t launch_chunk_tc(const Plan &, const int *, int, const void *, const 
                             cudaStream_t);
 
 // Device address of the status word, looked up once per device.
-static int *status_ptr() {
+int *status_ptr() {
     static PerDevice<int *> ptrs;
     const int dev = current_device();
     if (dev < 0) return nullptr;

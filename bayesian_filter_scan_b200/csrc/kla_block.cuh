@@ -107,6 +107,9 @@ __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-
 cudaError_t launch_colsum(const float *part, long long rows, long long cols, long long n0, float *out0, long long n1,
                           float *out1, float *out2, cudaStream_t st);
 
+// Device address of the library's status word on the current device (kla_api.cu).
+int *status_ptr();
+
 // ---- launch functions behind the C ABI ------------------------------------------
 
 struct ConvArgs {
@@ -151,6 +154,8 @@ struct SsmArgs {
     void *dx, *ddt, *dBm, *dCm, *dz;
     float *dA, *dDskip, *ddt_bias, *dstate0;
     float *part_bc;    // [tiles][2][N][ntok]
+    int *status;       // the library's device status word
+    int mode_x, mode_b;  // how rows of x, dt, z and of B, C are copied
     float *part_par;   // [nseq][D*N of dA, then D of dDskip, then D of ddt_bias]
 };
 cudaError_t launch_ssm_forward(const SsmArgs &, bool bf16, int sms, cudaStream_t);

@@ -301,6 +301,7 @@ kla_status kla_ssm_forward(const kla_ssm_desc *d, const void *x, const void *dt,
     b.out(states, ssm_state_records(g), 16, false);
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     if (g.ax.ntok == 0 && !final_state) return KLA_OK;
+    if (!(g.status = status_ptr())) return KLA_ERR_CUDA;
     return of_cuda(launch_ssm_forward(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
@@ -348,6 +349,7 @@ kla_status kla_ssm_backward(const kla_ssm_desc *d, const void *x, const void *dt
     char *p = (char *)ws;
     g.part_bc = (float *)(p + w.bc);
     g.part_par = (float *)(p + w.par);
+    if (!(g.status = status_ptr())) return KLA_ERR_CUDA;
     if (states) {
         g.states = const_cast<float *>(states);
     } else {
