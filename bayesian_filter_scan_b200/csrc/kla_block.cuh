@@ -98,8 +98,101 @@ __device__ __forceinline__ void store_v(T *p, const float (&x)[V]) {
     }
 }
 
-// Sigmoid through the accurate exponential; saturates without NaN.
-__device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
+// Sigmoid through the accurate exponential and an approximate quotient (2 units in
+// the last place); 0 where the exponential overflows.
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+
+// The same where the result is rounded to T: in bf16 the approximated power of two
+// (2^-22) and quotient stay far below its 2^-9 and cost a third.
+template <typename T>
+__device__ __forceinline__ float sigmoid_for(float x) {
+    if constexpr (sizeof(T) == 4) return sigmoid_f(x);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
+
+// V floats as pairs (the last one alone when V is 1).
+template <int V>
+struct Pairs {
+    static constexpr int K = (V + 1) / 2;
+    f32x2 p[K];
+    __device__ __forceinline__ void set(const float (&x)[V]) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) p[k] = pack2(x[2 * k], V > 1 ? x[V > 1 ? 2 * k + 1 : 0] : 0.f);
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float lo, hi;
+            unpack2(p[k], lo, hi);
+            x[2 * k] = lo;
+            if (V > 1) x[V > 1 ? 2 * k + 1 : 0] = hi;
+        }
+    }
+};
+// V contiguous values as they are in memory, one access; widened when they are used.
+template <int V, typename T>
+struct Raw {
+    static constexpr int K = V * (int)sizeof(T) / 4;      // words; 0: a single narrow element
+    uint32_t w[K ? K : 1];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (K == 4) {
+            const uint4 r = *reinterpret_cast<const uint4 *>(p);
+            w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+        } else if constexpr (K == 2) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(p);
+            w[0] = r.x; w[1] = r.y;
+        } else if constexpr (K == 1) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            w[0] = *reinterpret_cast<const unsigned short *>(p);
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = __uint_as_float(w[i]);
+        } else if constexpr (K == 0) {
+            x[0] = __uint_as_float(w[0] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
 
 // Sums part[rows][cols] over its rows in a fixed order: the first n0 columns go
 // to out0, the next n1 to out1, the others to out2; a NULL output is skipped
@@ -131,11 +224,11 @@ int conv_backward_blocks(long long ntok);
 cudaError_t launch_conv_backward(const ConvArgs &, bool bf16, float *dweight, float *dbias, cudaStream_t);
 cudaError_t launch_conv_step(const ConvArgs &, bool bf16, cudaStream_t);
 
-constexpr int kSsmCkpt = 128;     // tokens between two recorded states of a sequence
+constexpr int kSsmCkpt = 16;      // tokens between two recorded states of a sequence
 constexpr int kSsmMaxN = 128;
 
-// Index of sequence n's first recorded state: floor(s0 / 128) + n leaves room for
-// every earlier sequence's ceil(length / 128) records.
+// Index of sequence n's first recorded state: floor(s0 / 16) + n leaves room for
+// every earlier sequence's ceil(length / 16) records.
 __host__ __device__ inline long long ssm_ckpt_base(long long s0, int n) { return s0 / kSsmCkpt + n; }
 inline long long ssm_ckpt_count(long long ntok, int nseq) { return ntok / kSsmCkpt + nseq + 1; }
 
@@ -155,7 +248,7 @@ struct SsmArgs {
     float *dA, *dDskip, *ddt_bias, *dstate0;
     float *part_bc;    // [tiles][2][N][ntok]
     int *status;       // the library's device status word
-    int mode_x, mode_b;  // how rows of x, dt, z and of B, C are copied
+    int mode_x, mode_b, mode_s;  // how rows of x, dt, z (dout), of B, C, and of states are copied
     float *part_par;   // [nseq][D*N of dA, then D of dDskip, then D of ddt_bias]
 };
 cudaError_t launch_ssm_forward(const SsmArgs &, bool bf16, int sms, cudaStream_t);
@@ -180,7 +273,7 @@ struct NormArgs {
     void *dx;
     float *part;       // [ctas][2][D]
 };
-cudaError_t launch_norm_forward(const NormArgs &, bool bf16, cudaStream_t);
+cudaError_t launch_norm_forward(const NormArgs &, bool bf16, int sms, cudaStream_t);
 int norm_backward_ctas(long long rows, int D, int sms);
 cudaError_t launch_norm_backward(const NormArgs &, bool bf16, int ctas, float *dweight, float *dbias, cudaStream_t);
 

@@ -409,7 +409,7 @@ kla_status kla_layernorm_forward(const kla_norm_desc *d, const void *x, const vo
     b.out(mean, (size_t)g.rows * 4, 4, false);
     b.out(rstd, (size_t)g.rows * 4, 4, false);
     if (!b.good()) return KLA_ERR_INVALID_ARG;
-    return of_cuda(launch_norm_forward(g, d->dtype == KLA_BF16, st));
+    return of_cuda(launch_norm_forward(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
 size_t kla_layernorm_backward_workspace_bytes(const kla_norm_desc *d) {

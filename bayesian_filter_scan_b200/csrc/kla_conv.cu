@@ -14,10 +14,9 @@ namespace kla {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvRun = 16;      // tokens of one thread's run, forward
-constexpr int kConvBatch = 8;     // rows in flight per thread
-constexpr int kBwdRun = 32;       // tokens of one thread's run, backward
+constexpr int kBwdRun = 32;       // tokens of one thread's run, backward (the slacks of its sums count on it)
 constexpr int kBwdRuns = 8;       // runs per CTA
+constexpr int kBwdBatch = 4;      // rows in flight per thread, backward
 constexpr int kBwdLanes = 32;     // channel vectors per CTA
 
 // Row `back` places before token t of the sequence that starts at s0: x, or the
@@ -42,7 +41,7 @@ struct Taps {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = __ldg(g.w + (long long)(c + i) * W + k);
+            for (int k = 0; k < W; ++k) w[k][i] = __ldg(g.w + (c + i) * W + k);
             b[i] = g.bias ? __ldg(g.bias + c + i) : 0.f;
         }
     }
@@ -50,8 +49,8 @@ struct Taps {
 
 // Grid: (token blocks, then one block row per sequence for the final states) x
 // channel blocks; a CTA is bx channel vectors x 128 / bx runs.
-template <int W, int V, typename T>
-__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, long long tok_blocks) {
+template <int W, int V, int BATCH, typename T>
+__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, int run, long long tok_blocks) {
     const int cv = blockIdx.y * bx + threadIdx.x % bx, c = cv * V;
     if (c >= g.D) return;
     const T *x = static_cast<const T *>(g.x);
@@ -71,52 +70,79 @@ __global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvAr
         }
         return;
     }
-    long long t = ((long long)blockIdx.x * (kConvThreads / bx) + threadIdx.x / bx) * kConvRun;
-    const long long te = min(t + kConvRun, g.ax.ntok);
+    long long t = ((long long)blockIdx.x * (kConvThreads / bx) + threadIdx.x / bx) * run;
+    const long long te = min(t + run, g.ax.ntok);
     if (t >= te) return;
-    Taps<W, V> k;
-    k.load(g, c);
-    float win[W][V];          // rows t-(W-1) .. t
+    // a batch of rows is in flight while the one before is convolved
+    Raw<V, T> in[BATCH], next[BATCH];
+    auto load = [&](Raw<V, T>(&r)[BATCH], long long from) {
+        const T *p = x + from * g.ld_x + c;
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j, p += g.ld_x)
+            if (from + j < te) r[j].load(p);
+    };
+    load(in, t);
+    Pairs<V> w[W], bias, win[W];      // win: rows t-(W-1) .. t
+    {
+        Taps<W, V> k;
+        k.load(g, c);
+#pragma unroll
+        for (int r = 0; r < W; ++r) w[r].set(k.w[r]);
+        bias.set(k.b);
+    }
     int n = -1;
     long long s0 = 0, s1 = t;  // the current stretch of tokens ends at s1
-    for (; t < te; t += kConvBatch) {
-        float in[kConvBatch][V];
+    T *out = static_cast<T *>(g.out) + t * g.D + c;
+    // one token; `inside`: known to lie in the current sequence
+    auto token = [&](const Raw<V, T> &r, long long tj, auto inside) {
+        if (!inside.value && tj >= s1) {
+            n = g.ax.find(tj);
+            if (n >= 0) {
+                g.ax.range(n, s0, s1);
 #pragma unroll
-        for (int j = 0; j < kConvBatch; ++j)
-            if (t + j < te) load_v<V>(x + (t + j) * g.ld_x + c, in[j]);
-#pragma unroll
-        for (int j = 0; j < kConvBatch; ++j) {
-            const long long tj = t + j;
-            if (tj >= te) break;
-            if (tj >= s1) {
-                n = g.ax.find(tj);
-                if (n >= 0) {
-                    g.ax.range(n, s0, s1);
-#pragma unroll
-                    for (int r = 0; r < W - 1; ++r) row_before<W, V, T>(g, n, s0, tj - (W - 1) + r, c, win[r]);
-                } else {
-                    s1 = tj + 1;
+                for (int i = 0; i < W - 1; ++i) {
+                    float f[V];
+                    row_before<W, V, T>(g, n, s0, tj - (W - 1) + i, c, f);
+                    win[i].set(f);
                 }
+            } else {
+                s1 = tj + 1;
             }
-            if (n < 0) continue;
-            float y[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                win[W - 1][i] = in[j][i];
-                float a = k.b[i];
-#pragma unroll
-                for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
-                y[i] = g.silu ? a * sigmoid_f(a) : a;
-#pragma unroll
-                for (int r = 0; r < W - 1; ++r) win[r][i] = win[r + 1][i];
-            }
-            store_v<V>(static_cast<T *>(g.out) + tj * g.D + c, y);
         }
+        if (!inside.value && n < 0) return;
+        float y[V];
+        r.get(y);
+        win[W - 1].set(y);
+        Pairs<V> a = bias;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int k = 0; k < Pairs<V>::K; ++k) a.p[k] = fma2(w[i].p[k], win[i].p[k], a.p[k]);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) win[i] = win[i + 1];
+        a.get(y);
+        if (g.silu)
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] *= sigmoid_for<T>(y[i]);
+        store_v<V>(out, y);
+    };
+    for (; t < te; t += BATCH) {
+        load(next, t + BATCH);
+        if (n >= 0 && t + BATCH <= min(te, s1)) {
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j, out += g.D) token(in[j], t + j, std::true_type());
+        } else {
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j, out += g.D)
+                if (t + j < te) token(in[j], t + j, std::false_type());
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) in[j] = next[j];
     }
 }
 
 // d = dout * silu'(pre) of one token
-template <int W, int V>
+template <typename T, int W, int V>
 __device__ __forceinline__ void d_pre(const ConvArgs &g, const Taps<W, V> &k, const float (&win)[W][V],
                                       const float (&dout)[V], float (&d)[V]) {
 #pragma unroll
@@ -126,7 +152,7 @@ __device__ __forceinline__ void d_pre(const ConvArgs &g, const Taps<W, V> &k, co
             float a = k.b[i];
 #pragma unroll
             for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
-            const float s = sigmoid_f(a);
+            const float s = sigmoid_for<T>(a);
             d[i] *= s * fmaf(a, 1.f - s, 1.f);
         }
     }
@@ -169,33 +195,31 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(con
             }
             store_v<V>(static_cast<T *>(g.dx) + p * g.D + c, v);
         };
-        for (long long t = a;; ++t) {
-            if (t >= s1) {
-                if (t >= b) break;
-                n = g.ax.find(t);
-                if (n < 0) {
-                    s1 = t + 1;
-                    continue;
-                }
-                g.ax.range(n, s0, s1);
+        // a batch of rows is in flight while the one before is worked on
+        const long long te = min(b + (W - 1), g.ax.ntok);
+        Raw<V, T> bx[kBwdBatch], bo[kBwdBatch], nx[kBwdBatch], no[kBwdBatch];
+        auto load = [&](Raw<V, T>(&rx)[kBwdBatch], Raw<V, T>(&ro)[kBwdBatch], long long from) {
 #pragma unroll
-                for (int r = 0; r < W - 1; ++r) {
-                    row_before<W, V, T>(g, n, s0, t - (W - 1) + r, c, win[r]);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) acc[r][i] = 0.f;
+            for (int j = 0; j < kBwdBatch; ++j)
+                if (from + j < te) {
+                    rx[j].load(x + (from + j) * g.ld_x + c);
+                    ro[j].load(dout + (from + j) * g.D + c);
                 }
-            }
+        };
+        load(bx, bo, a);
+        // one token of the sequence; `inside`: neither near an end of the run nor of the sequence
+        auto token = [&](const Raw<V, T> &rx, const Raw<V, T> &ro, long long t, auto inside) {
             float o[V], d[V];
-            load_v<V>(x + t * g.ld_x + c, win[W - 1]);
-            load_v<V>(dout + t * g.D + c, o);
-            d_pre<W, V>(g, k, win, o, d);
+            rx.get(win[W - 1]);
+            ro.get(o);
+            d_pre<T, W, V>(g, k, win, o, d);
 #pragma unroll
-            for (int j = W - 1; j > 0; --j)
+            for (int q = W - 1; q > 0; --q)
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[j][i] = fmaf(k.w[W - 1 - j][i], d[i], acc[j - 1][i]);
+                for (int i = 0; i < V; ++i) acc[q][i] = fmaf(k.w[W - 1 - q][i], d[i], acc[q - 1][i]);
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[0][i] = k.w[W - 1][i] * d[i];
-            if (t < b) {
+            if (inside.value || t < b) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     db[i] += d[i];
@@ -207,15 +231,51 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(con
             for (int r = 0; r < W - 1; ++r)
 #pragma unroll
                 for (int i = 0; i < V; ++i) win[r][i] = win[r + 1][i];
-            // token t-(W-1) is complete; at the sequence's end (or the halo's) so are the ones behind it
+            if (inside.value) {
+                store_v<V>(static_cast<T *>(g.dx) + (t - (W - 1)) * g.D + c, acc[W - 1]);
+                return;
+            }
+            // token t-(W-1) is complete; at the sequence's end so are the ones behind it
             const long long lo = max(a, s0);
             if (t - (W - 1) >= lo) put(t - (W - 1), acc[W - 1]);
             if (t + 1 == s1) {
 #pragma unroll
-                for (int j = W - 2; j >= 0; --j)
-                    if (t - j >= lo && t - j < b) put(t - j, acc[j]);
+                for (int q = W - 2; q >= 0; --q)
+                    if (t - q >= lo && t - q < b) put(t - q, acc[q]);
             }
-            if (t + 1 >= b + (W - 1)) break;
+        };
+        bool more = true;
+        for (long long t0 = a; more && t0 < te; t0 += kBwdBatch) {
+            load(nx, no, t0 + kBwdBatch);
+            if (n >= 0 && t0 - (W - 1) >= max(a, s0) && t0 + kBwdBatch <= b && t0 + kBwdBatch < s1) {
+#pragma unroll
+                for (int j = 0; j < kBwdBatch; ++j) token(bx[j], bo[j], t0 + j, std::true_type());
+            } else {
+#pragma unroll
+                for (int j = 0; j < kBwdBatch; ++j) {
+                    const long long t = t0 + j;
+                    // tokens behind the run only as far as its last sequence goes
+                    if (t >= te || (t >= s1 && t >= b)) more = false;
+                    if (!more) continue;
+                    if (t >= s1) {
+                        n = g.ax.find(t);
+                        if (n < 0) {
+                            s1 = t + 1;
+                            continue;
+                        }
+                        g.ax.range(n, s0, s1);
+#pragma unroll
+                        for (int r = 0; r < W - 1; ++r) {
+                            row_before<W, V, T>(g, n, s0, t - (W - 1) + r, c, win[r]);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) acc[r][i] = 0.f;
+                        }
+                    }
+                    if (n >= 0) token(bx[j], bo[j], t, std::false_type());
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBwdBatch; ++j) bx[j] = nx[j], bo[j] = no[j];
         }
     }
 #pragma unroll
@@ -264,7 +324,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_dstate_kernel(const ConvArg
                 float o[1], d[1];
                 load_v<1>(static_cast<const T *>(g.x) + (s0 + p) * g.ld_x + c, win[W - 1]);
                 load_v<1>(static_cast<const T *>(g.dout) + (s0 + p) * g.D + c, o);
-                d_pre<W, 1>(g, k, win, o, d);
+                d_pre<T, W, 1>(g, k, win, o, d);
 #pragma unroll
                 for (int i = p; i < W - 1; ++i) ds[i] = fmaf(k.w[i - p][0], d[0], ds[i]);
 #pragma unroll
@@ -296,7 +356,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvArgs 
         float a = k.b[i];
 #pragma unroll
         for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
-        y[i] = g.silu ? a * sigmoid_f(a) : a;
+        y[i] = g.silu ? a * sigmoid_for<T>(a) : a;
     }
     store_v<V>(static_cast<T *>(g.out) + n * g.D + c, y);
 #pragma unroll
@@ -313,18 +373,22 @@ bool rows_aligned(const ConvArgs &g, int es, size_t a) {
     return ((size_t)g.D * es) % a == 0 && ((size_t)g.ld_x * es) % a == 0;
 }
 
-template <int W, int V, typename T>
+template <int W, int V, int BATCH, typename T>
 cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
     const int nvec = (g.D + V - 1) / V;
     int bx = 1;
     while (bx < nvec && bx < kConvThreads) bx *= 2;
     const int runs = kConvThreads / bx;
-    const long long tok_blocks = (g.ax.ntok + (long long)runs * kConvRun - 1) / ((long long)runs * kConvRun);
+    // long runs load the taps, the rows in front of them and their sequence's offsets less
+    // often; short ones fill the SMs
+    int run = 64;
+    while (run > BATCH && nvec * (g.ax.ntok / run) < 148LL * 1024) run /= 2;
+    const long long tok_blocks = (g.ax.ntok + (long long)runs * run - 1) / ((long long)runs * run);
     const long long seq_blocks = (W > 1 && g.final_state) ? (g.ax.nseq + runs - 1) / runs : 0;
     if (tok_blocks + seq_blocks == 0) return cudaSuccess;
     if (tok_blocks + seq_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(tok_blocks + seq_blocks), (unsigned)((nvec + bx - 1) / bx));
-    conv_forward_kernel<W, V, T><<<grid, kConvThreads, 0, st>>>(g, bx, tok_blocks);
+    conv_forward_kernel<W, V, BATCH, T><<<grid, kConvThreads, 0, st>>>(g, bx, run, tok_blocks);
     return cudaGetLastError();
 }
 
@@ -358,8 +422,10 @@ enum class Call { kForward, kBackward, kStep };
 template <int W, typename T>
 cudaError_t conv_w(const ConvArgs &g, Call call, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    const bool vec = rows_aligned(g, sizeof(T), call == Call::kBackward ? 8 : 16);
-    if (call == Call::kForward) return vec ? forward_t<W, V, T>(g, st) : forward_t<W, 1, T>(g, st);
+    const bool vec = rows_aligned(g, sizeof(T), call == Call::kStep ? 16 : 8);
+    // 8-byte accesses, four rows ahead: 80 registers (32768 tokens of 2048 channels 70 us;
+    // 78 eight rows ahead, 85 and 93 with 16-byte accesses, whose registers halve the warps)
+    if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, st) : forward_t<W, 1, 8, T>(g, st);
     if (call == Call::kStep) return vec ? step_t<W, V, T>(g, st) : step_t<W, 1, T>(g, st);
     // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers
     return vec ? backward_t<W, V / 2, T>(g, st) : backward_t<W, 1, T>(g, st);

@@ -15,11 +15,12 @@
 // two, all of them busy, each decay computed and used once, and nothing walked
 // twice. A warp keeps steps, inputs and outputs of its tile in registers.
 //
-// Backward: a CTA owns 16 channels and walks chunks of 128 tokens. A thread has a
-// channel and a range of 8 tokens; per state the ranges' maps of the start state
-// (decay product, end state from zero) are joined within and across warps, and the
-// adjoint's maps from the right in the same way; the thread then replays its tokens
-// with the same decays.
+// Backward: the same tiles from the last to the first, the adjoint a_{t+1} dh_{t+1}
+// handed from warp to warp. The forward call records the state before every tile, so a
+// warp walks its tile's states forward and then the adjoint backward with one set of
+// decays. dB and dC are sums over channels: a transposing reduction over the warp's
+// channels leaves each lane one token's sum, and a second kernel adds the channel tiles
+// in a fixed order.
 #include <initializer_list>
 
 #include "kla_block.cuh"
@@ -28,11 +29,9 @@ namespace kla {
 
 namespace {
 
-constexpr int kFwdL = 16;        // tokens of a tile, forward
-constexpr int kFwdNB = 16;       // states whose B and C a warp stages at once
-constexpr int kBwdWarps = 8;
-constexpr int kBwdL = 8;         // tokens per thread, backward
-constexpr int kLdPad = 4;        // floats behind a range's tokens in shared memory: ranges on other banks
+constexpr int kTileL = 16;       // tokens of a tile
+constexpr int kTileNB = 16;      // states whose B and C a warp stages at once
+constexpr int kLdPad = 4;        // floats behind a state's tokens in shared memory: states on other banks
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -45,29 +44,6 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// Two fp32 values in one 64-bit register: one instruction for both.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
 
 // softplus(x) = max(x, 0) + log(1 + y) of two values, y = e^-|x| in (0, 1]. log(1 + y)
 // is y times a polynomial of degree 9 fitted to log(1 + y) / y on [0, 1] for the least
@@ -135,21 +111,6 @@ __device__ __forceinline__ void copy_rows(T *dst, const T *src, long long ld, in
     }
 }
 
-// A chunk: ranges of L tokens, 32/CB per warp. B and C of a chunk stand in shared
-// memory as [state][range][L + pad] fp32: a thread reads its tokens as 16-byte
-// vectors, the lanes of one range the same address. The state stride is 4 floats
-// off a multiple of the banks, for the writes of several states of one token.
-template <int CB, int L, int WARPS>
-struct Tile {
-    static constexpr int kNB = CB <= 8 ? 8 : 16;            // states staged at once
-    static constexpr int kSub = 32 / CB;                    // ranges per warp
-    static constexpr int kRanges = WARPS * kSub;            // ranges per chunk
-    static constexpr int kTok = kRanges * L;                // tokens per chunk
-    static constexpr int kRow = L + kLdPad;                 // floats per range
-    static constexpr int kState = kRanges * kRow + 4;       // floats per state
-    static __device__ __forceinline__ int at(int n, int t) { return n * kState + (t / L) * kRow + t % L; }
-};
-
 // The unit of a CTA: sequence and channel tile; tiles do not straddle groups.
 struct Unit {
     int n, tile, group, c0, live;     // c0: the tile's first channel; live: its channels
@@ -167,12 +128,57 @@ __device__ __forceinline__ Unit unit_of(const SsmArgs &g) {
     return u;
 }
 
+// A staged block of B (half the warp) and C (the other half) as fp32 [state][kRow];
+// zero behind the sequence's end and the last state.
+template <int NB, int ROW, typename T>
+__device__ __forceinline__ void widen(float *sB, float *sC, const T *raw, int have, int states, int lane) {
+    constexpr int L = kTileL, V = 16 / (int)sizeof(T), PR = NB / V;
+    const int t = lane % L, which = lane / L;
+    float *dst = (which ? sC : sB) + t;
+    const T *src = raw + which * L * NB + t * NB;
+    float v[PR][V];
+#pragma unroll
+    for (int k = 0; k < PR; ++k) load_v<V>(src + k * V, v[k]);
+    if (have < L || states < NB) {
+#pragma unroll
+        for (int k = 0; k < PR; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (t >= have || k * V + i >= states) v[k][i] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < PR; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dst[(k * V + i) * ROW] = v[k][i];
+}
+
+// Adds up v over the lanes that differ in the bits FROM .. TO (powers of two, falling),
+// halving the values at each: a lane ends with COUNT >> bits of them, chosen by its
+// bits, the highest bit the upper half.
+template <int FROM, int TO, int COUNT, int M>
+__device__ __forceinline__ void reduce_halving(float (&v)[M], int lane) {
+    int count = COUNT;
+#pragma unroll
+    for (int o = FROM; o >= TO; o >>= 1) {
+        count >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int j = 0; j < COUNT / 2; ++j) {
+            if (j < count) {
+                const float send = up ? v[j] : v[j + count];
+                const float keep = up ? v[j + count] : v[j];
+                v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+    }
+}
+
 // Shared memory of the forward kernel: per warp two stages of a tile's rows (x, dt,
 // z) and of a block of B and C, that block as fp32 [state][token + pad], and the
 // words through which the tile before hands over its states; per CTA A * log2(e).
 template <int CB, typename T>
 struct FwdSmem {
-    static constexpr int L = kFwdL, NB = kFwdNB, NS = 32 / CB;
+    static constexpr int L = kTileL, NB = kTileNB, NS = 32 / CB;
     static constexpr int kRow = L + kLdPad;
     static constexpr size_t rows = 3 * (size_t)L * CB * sizeof(T);
     static constexpr size_t raw = 2 * (size_t)L * NB * sizeof(T);
@@ -233,29 +239,6 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
         if (OUT)
             copy_rows<L, NB, 32>(b + L * NB, Cm + (long long)tile * L * g.ld_c + n0, g.ld_c, have, states, g.mode_b, lane);
     };
-    // The staged block of B (half the warp) and C (the other half) as fp32; zero behind
-    // the sequence's end and the last state.
-    auto widen = [&](const T *raw, int have, int states) {
-        constexpr int V = 16 / (int)sizeof(T), PR = NB / V;
-        const int t = lane % L, which = lane / L;
-        float *dst = (which ? sC : sB) + t;
-        const T *src = raw + which * L * NB + t * NB;
-        float v[PR][V];
-#pragma unroll
-        for (int k = 0; k < PR; ++k) load_v<V>(src + k * V, v[k]);
-        if (have < L || states < NB) {
-#pragma unroll
-            for (int k = 0; k < PR; ++k)
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (t >= have || k * V + i >= states) v[k][i] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < PR; ++k)
-#pragma unroll
-            for (int i = 0; i < V; ++i) dst[(k * V + i) * M::kRow] = v[k][i];
-    };
-
     if (warp < tiles) fetch(warp, 0, 0, 0);
     cp_async_commit();
     const int padded = M::padded(g.N);
@@ -294,7 +277,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
             const int states = min(NB, g.N - n0);
             cp_async_wait();
             __syncwarp();
-            widen(raw_at(half), have, states);
+            widen<NB, M::kRow>(sB, sC, raw_at(half), have, states, lane);
             if (n0 + NB < g.N) fetch(tile, n0 + NB, rh, half ^ 1);
             else if (tile + warps < tiles) fetch(tile + warps, 0, rh ^ 1, half ^ 1);
             cp_async_commit();
@@ -418,20 +401,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
 #pragma unroll
             for (int i = 0; i < L / 2; ++i) unpack2(y[i], v[2 * i], v[2 * i + 1]);
             // the states' lanes add up, each keeping its share of the tokens
-            int count = L;
-#pragma unroll
-            for (int o = 16; o >= CB; o >>= 1) {
-                count >>= 1;
-                const bool up = lane & o;
-#pragma unroll
-                for (int j = 0; j < L / 2; ++j) {
-                    if (j < count) {
-                        const float send = up ? v[j] : v[j + count];
-                        const float keep = up ? v[j + count] : v[j];
-                        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                    }
-                }
-            }
+            reduce_halving<16, CB, L>(v, lane);
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
                 v[i] = fmaf(skip, xs[i], v[i]);
@@ -447,277 +417,347 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
     }
 }
 
-// Sums v[16] over the CB channel lanes of a range, by halving: after step o a lane
-// holds half as many values, each the sum of twice as many lanes. Lane lc ends
-// with values lc * 16/CB + j, j < 16/CB.
-template <int CB>
-__device__ __forceinline__ void sum_over_channels(float (&v)[16], int lc) {
-    int count = 16;
-#pragma unroll
-    for (int o = CB / 2; o > 0; o >>= 1) {
-        count >>= 1;
-        const bool up = lc & o;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j < count) {
-                const float send = up ? v[j] : v[j + count];
-                const float keep = up ? v[j + count] : v[j];
-                v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
-        }
-    }
-}
-
-constexpr int kBwdThreads = kBwdWarps * 32;
-
-// States [n0, n0 + S::kNB) of the chunk's rows of B or C into shared memory as fp32.
-template <int CB, int L, typename T>
-__device__ __forceinline__ void stage(float *dst, const T *src, long long ld, long long t0, long long t1, int n0,
-                                      int N) {
-    using S = Tile<CB, L, kBwdWarps>;
-    for (int e = threadIdx.x; e < S::kTok * S::kNB; e += kBwdThreads) {
-        const int n = e % S::kNB, t = e / S::kNB;
-        float v = 0.f;
-        if (n0 + n < N && t0 + t < t1) v = to_f(src[(t0 + t) * ld + n0 + n]);
-        dst[S::at(n, t)] = v;
-    }
-}
-
-template <int CB>
+// Shared memory of the backward kernel: per warp two stages of a tile's rows (x, dt,
+// dout, z), of a block of B and C and of that block's start states, B and C as fp32,
+// the words of the adjoint, and the sums of dA, dDskip and ddt_bias; per CTA A.
+template <int CB, typename T>
 struct BwdSmem {
-    static __host__ __device__ size_t bytes(int N) {
-        using S = Tile<CB, kBwdL, kBwdWarps>;
-        // B, C; the adjoint's carry (two halves); exchange; dA and the two channel sums per warp
-        return sizeof(float) * (2 * (size_t)S::kNB * S::kState + 2 * (size_t)N * CB + 2 * 4 * kBwdWarps * CB +
-                                (size_t)kBwdWarps * (N + 2) * CB);
-    }
+    static constexpr int L = kTileL, NB = kTileNB, NS = 32 / CB;
+    static constexpr int kRow = L + kLdPad, kC = NB * kRow + 16;
+    static constexpr size_t rows = 4 * (size_t)L * CB * sizeof(T);
+    static constexpr size_t raw = 2 * (size_t)L * NB * sizeof(T);
+    static constexpr size_t start = (size_t)NB * CB * sizeof(float);
+    static constexpr size_t wide = (kC + (size_t)NB * kRow) * sizeof(float);
+    static constexpr size_t words = 2 * (rows + raw + start) + wide;
+    static __host__ __device__ int padded(int N) { return (N + NS - 1) / NS * NS; }
+    static __host__ __device__ size_t sums(int N) { return words + (size_t)padded(N) * CB * 8; }
+    static __host__ __device__ size_t warp(int N) { return sums(N) + (size_t)(padded(N) + 2) * CB * 4; }
+    static size_t bytes(int N, int warps) { return warps * warp(N) + (size_t)padded(N) * CB * sizeof(float); }
 };
 
-// Chunks from the last to the first. Per state: decays, the forward walk from the
-// recorded state before the chunk, the adjoint walk dh_t = C_t g_t + a_{t+1} dh_{t+1}
-// (g: the gradient at y) whose incoming value joins from the right, and the sums
-// over channels of dh delta x (dB) and g h (dC), which leave as the tile's partial
-// sums: a second kernel adds the tiles in a fixed order.
-template <int CB, typename T>
-__global__ void __launch_bounds__(kBwdThreads, 2) ssm_backward_kernel(const SsmArgs g) {
-    constexpr int L = kBwdL;
-    using S = Tile<CB, L, kBwdWarps>;
-    static_assert(S::kTok % kSsmCkpt == 0, "chunks start at recorded states");
-    extern __shared__ __align__(16) float sm[];
-    float *sB = sm, *sC = sB + S::kNB * S::kState;
-    float4 *exch = reinterpret_cast<float4 *>(sC + S::kNB * S::kState);    // [2][warps][CB]
-    float *carry = reinterpret_cast<float *>(exch + 2 * kBwdWarps * CB);    // [2][N][CB]
-    float *sA = carry + 2 * g.N * CB;                                       // [warps][N + 2][CB]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lc = lane % CB, sub = lane / CB;
-    const int range = warp * S::kSub + sub;
+// GATE: z was given. blockDim is (32, warps); a warp's p-th tile from the end.
+template <int CB, bool GATE, typename T>
+__global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
+    using M = BwdSmem<CB, T>;
+    constexpr int L = M::L, NB = M::NB, NS = M::NS, LS = L / NS;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x, warp = threadIdx.y, warps = blockDim.y, lc = lane % CB, ls = lane / CB;
+    unsigned char *mine = smem + warp * M::warp(g.N);
+    auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };                  // [4][L][CB]
+    auto raw_at = [&](int half) { return reinterpret_cast<T *>(mine + 2 * M::rows + half * M::raw); };       // [2][L][NB]
+    auto start_at = [&](int half) {                                                                          // [NB][CB]
+        return reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw) + half * M::start);
+    };
+    float *sB = reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw + M::start)), *sC = sB + M::kC;       // [NB][kRow]
+    auto words_of = [&](int w) {                                                                             // [N][CB]
+        return reinterpret_cast<volatile unsigned long long *>(smem + w * M::warp(g.N) + M::words);
+    };
+    auto sums_of = [&](int w) { return reinterpret_cast<float *>(smem + w * M::warp(g.N) + M::sums(g.N)); };  // [N + 2][CB]
+    float *sA = reinterpret_cast<float *>(smem + warps * M::warp(g.N));                                       // [N][CB]
     const Unit u = unit_of<CB>(g);
     long long s0, s1;
     g.ax.range(u.n, s0, s1);
     const bool live = lc < u.live;
     const int c = u.c0 + (live ? lc : 0);
-    const T *x = static_cast<const T *>(g.x) + c, *dt = static_cast<const T *>(g.dt) + c;
-    const T *z = g.z ? static_cast<const T *>(g.z) + c : nullptr;
-    const T *dout = static_cast<const T *>(g.dout) + c;
-    const T *Bm = static_cast<const T *>(g.Bm) + (long long)u.group * g.N;
-    const T *Cm = static_cast<const T *>(g.Cm) + (long long)u.group * g.N;
+    const T *x = static_cast<const T *>(g.x) + s0 * g.ld_x + u.c0;
+    const T *dt = static_cast<const T *>(g.dt) + s0 * g.ld_dt + u.c0;
+    const T *z = GATE ? static_cast<const T *>(g.z) + s0 * g.ld_z + u.c0 : nullptr;
+    const T *dout = static_cast<const T *>(g.dout) + s0 * g.D + u.c0;
+    const T *Bm = static_cast<const T *>(g.Bm) + s0 * g.ld_b + (long long)u.group * g.N;
+    const T *Cm = static_cast<const T *>(g.Cm) + s0 * g.ld_c + (long long)u.group * g.N;
+    const float *states0 = g.states + ssm_ckpt_base(s0, u.n) * g.N * g.D + u.c0;
     const float bias = g.dt_bias ? g.dt_bias[c] : 0.f, skip = g.Dskip ? g.Dskip[c] : 0.f;
-    const float *A = g.A + (long long)c * g.N;
+    const int len = (int)(s1 - s0), tiles = (int)(((long long)len + L - 1) / L);
     float *part = g.part_bc + (long long)u.tile * 2 * g.N * g.ax.ntok;
-    for (int e = threadIdx.x; e < g.N * CB; e += kBwdThreads) {
-        const int n = e % g.N, j = e / g.N;
-        const int ch = j < u.live ? u.c0 + j : -1;
-        carry[n * CB + j] = (g.dfinal && ch >= 0) ? g.dfinal[((long long)u.n * g.D + ch) * g.N + n] : 0.f;
+
+    auto fetch = [&](int tile, int n0, int rh, int half) {
+        const int have = min(L, len - tile * L), states = min(NB, g.N - n0);
+        const long long t = (long long)tile * L;
+        T *r = rows_at(rh), *b = raw_at(half);
+        if (n0 == 0) {
+            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, g.mode_x, lane);
+            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, g.mode_x, lane);
+            copy_rows<L, CB, 32>(r + 2 * L * CB, dout + t * g.D, g.D, have, u.live, g.mode_x, lane);
+            if (GATE) copy_rows<L, CB, 32>(r + 3 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, g.mode_x, lane);
+        }
+        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, g.mode_b, lane);
+        copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, g.mode_b, lane);
+        copy_rows<NB, CB, 32>(start_at(half), states0 + ((long long)tile * g.N + n0) * g.D, g.D, states, u.live, g.mode_s,
+                              lane);
+    };
+
+    if (warp < tiles) fetch(tiles - 1 - warp, 0, 0, 0);
+    cp_async_commit();
+    const int padded = M::padded(g.N);
+    for (int e = warp * 32 + lane; e < padded * CB; e += warps * 32) {
+        const int n = e % padded, j = e / padded;
+        float a = 0.f, q = 0.f;
+        if (j < u.live && n < g.N) {
+            const long long at = ((long long)u.n * g.D + u.c0 + j) * g.N + n;
+            a = g.A[(long long)(u.c0 + j) * g.N + n];
+            if (g.dfinal) q = g.dfinal[at];
+            if (tiles == 0 && g.dstate0) g.dstate0[at] = q;
+        }
+        sA[n * CB + j] = a;
+        for (int w = 0; w < warps; ++w) {
+            words_of(w)[n * CB + j] = w ? 0xffffffff00000000ull : (unsigned long long)__float_as_uint(q);
+            sums_of(w)[n * CB + j] = 0.f;
+        }
     }
-    for (int e = threadIdx.x; e < kBwdWarps * (g.N + 2) * CB; e += kBwdThreads) sA[e] = 0.f;
+    __syncthreads();
     float sumD = 0.f, sumT = 0.f;
-    int par = 0, xp = 0;
-    const long long chunks = (s1 - s0 + S::kTok - 1) / S::kTok;
-    for (long long k = chunks - 1; k >= 0; --k, par ^= 1) {
-        const long long t0 = s0 + k * S::kTok, tk = t0 + range * L;
-        float del[L], dx[L], go[L], ddel[L], du[L], y[L], sum = 0.f;
+    int rh = 0, half = 0;
+    for (int p = warp; p < tiles; p += warps, rh ^= 1) {
+        const int tile = tiles - 1 - p, have = min(L, len - tile * L);
+        const T *rx = rows_at(rh) + lc;
+        f32x2 del[L / 2], dx[L / 2], go[L / 2], ddel[L / 2], du[L / 2], y[L / 2];
+        for (int n0 = 0; n0 < g.N; n0 += NB, half ^= 1) {
+            const int states = min(NB, g.N - n0);
+            cp_async_wait();
+            __syncwarp();
+            widen<NB, M::kRow>(sB, sC, raw_at(half), have, states, lane);
+            if (n0 + NB < g.N) fetch(tile, n0 + NB, rh, half ^ 1);
+            else if (p + warps < tiles) fetch(tile - warps, 0, rh ^ 1, half ^ 1);
+            cp_async_commit();
+            if (n0 == 0) {
+                // a lane's share of the tile's tokens
+                float d[LS], w[LS], o[LS];
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            del[i] = dx[i] = go[i] = ddel[i] = du[i] = y[i] = 0.f;
-            if (live && tk + i < s1) {
-                float r = to_f(dt[(tk + i) * g.ld_dt]) + bias, unused = 0.f;
-                if (g.softplus) softplus2(r, unused);
-                del[i] = r;
-                dx[i] = del[i] * to_f(x[(tk + i) * g.ld_x]);
-                go[i] = to_f(dout[(tk + i) * g.D]);
-                if (z) {
-                    const float zz = to_f(z[(tk + i) * g.ld_z]);
-                    go[i] *= zz * sigmoid_f(zz);
-                }
-            }
-            sum += del[i];
-        }
-        const float *ck = g.states + (ssm_ckpt_base(s0, u.n) + k * (S::kTok / kSsmCkpt)) * g.N * g.D + c;
-        for (int n0 = 0; n0 < g.N; n0 += S::kNB) {
-            __syncthreads();
-            stage<CB, L>(sB, Bm, g.ld_b, t0, s1, n0, g.N);
-            stage<CB, L>(sC, Cm, g.ld_c, t0, s1, n0, g.N);
-            __syncthreads();
-            const int n1 = min(n0 + S::kNB, g.N);
-            for (int n = n0; n < n1; ++n, xp ^= 1) {
-                const float An = A[n], A2 = An * kLog2e;
-                const float start = live ? ck[(long long)n * g.D] : 0.f;
-                const float *bp = sB + S::at(n - n0, range * L), *cp = sC + S::at(n - n0, range * L);
-                float a[L], H = 0.f, Q = 0.f;
-#pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    a[i] = ex2(del[i] * A2);
-                    H = fmaf(a[i], H, dx[i] * bp[i]);
-                }
-#pragma unroll
-                for (int i = L - 1; i >= 0; --i) Q = a[i] * fmaf(cp[i], go[i], Q);
-                const float P = ex2(sum * A2);
-                // maps of the warp's earlier ranges (forward) and later ranges (adjoint)
-                float pf = P, pb = P;
-#pragma unroll
-                for (int o = 1; o < S::kSub; o *= 2) {
-                    const float p = __shfl_up_sync(0xffffffffu, pf, o * CB), h = __shfl_up_sync(0xffffffffu, H, o * CB);
-                    if (sub >= o) {
-                        H = fmaf(pf, h, H);
-                        pf *= p;
-                    }
-                    const float r = __shfl_down_sync(0xffffffffu, pb, o * CB), q = __shfl_down_sync(0xffffffffu, Q, o * CB);
-                    if (sub + o < S::kSub) {
-                        Q = fmaf(pb, q, Q);
-                        pb *= r;
+                for (int i = 0; i < LS; ++i) {
+                    const int t = ls * LS + i;
+                    w[i] = to_f(rx[t * CB]);
+                    d[i] = to_f(rx[(L + t) * CB]) + bias;
+                    o[i] = to_f(rx[(2 * L + t) * CB]);
+                    if (GATE) {
+                        const float zz = to_f(rx[(3 * L + t) * CB]);
+                        o[i] *= zz * sigmoid_a(zz);
                     }
                 }
-                float4 *ex = exch + (xp * kBwdWarps + warp) * CB + lc;
-                if (sub == S::kSub - 1) ex->x = pf, ex->y = H;
-                if (sub == 0) ex->z = Q;
-                if constexpr (S::kSub > 1) {
-                    pf = __shfl_up_sync(0xffffffffu, pf, CB);
-                    H = __shfl_up_sync(0xffffffffu, H, CB);
-                    pb = __shfl_down_sync(0xffffffffu, pb, CB);
-                    Q = __shfl_down_sync(0xffffffffu, Q, CB);
-                }
-                if (sub == 0) pf = 1.f, H = 0.f;
-                if (sub == S::kSub - 1) pb = 1.f, Q = 0.f;
-                __syncthreads();
-                float h = start, q = carry[(par * g.N + n) * CB + lc];
-                for (int w = 0; w < warp; ++w) {
-                    const float4 e = exch[(xp * kBwdWarps + w) * CB + lc];
-                    h = fmaf(e.x, h, e.y);
-                }
-                for (int w = kBwdWarps - 1; w > warp; --w) {
-                    const float4 e = exch[(xp * kBwdWarps + w) * CB + lc];
-                    q = fmaf(e.x, q, e.z);
-                }
-                h = fmaf(pf, h, H);
-                q = fmaf(pb, q, Q);
-                float hs[L + 1], v[16];
-                hs[0] = h;
+                if (g.softplus) {
 #pragma unroll
-                for (int i = 0; i < L; ++i) {
-                    hs[i + 1] = fmaf(a[i], hs[i], dx[i] * bp[i]);
-                    y[i] = fmaf(cp[i], hs[i + 1], y[i]);
-                    v[8 + i] = go[i] * hs[i + 1];
+                    for (int i = 0; i < LS; i += 2) softplus2(d[i], d[i + 1]);
                 }
-                float dA = 0.f;
 #pragma unroll
-                for (int i = L - 1; i >= 0; --i) {
-                    const float dh = fmaf(cp[i], go[i], q);
-                    v[i] = dh * dx[i];
-                    du[i] = fmaf(dh, bp[i], du[i]);
-                    q = a[i] * dh;
-                    const float m = q * hs[i];         // dL/d(delta A)
-                    ddel[i] = fmaf(m, An, ddel[i]);
-                    dA = fmaf(m, del[i], dA);
+                for (int i = 0; i < LS; ++i) w[i] *= d[i];
+                if (have < L || u.live < CB) {
+                    // behind the end, and channels of no one: step 0, so decay 1, input 0, gradient 0
+#pragma unroll
+                    for (int i = 0; i < LS; ++i)
+                        if (!live || ls * LS + i >= have) d[i] = w[i] = o[i] = 0.f;
                 }
-                if (range == 0) carry[((par ^ 1) * g.N + n) * CB + lc] = q;
 #pragma unroll
-                for (int o = CB; o < 32; o *= 2) dA += __shfl_xor_sync(0xffffffffu, dA, o);
-                if (sub == 0) sA[(warp * (g.N + 2) + n) * CB + lc] += dA;
-                // dead lanes hold zeros: their steps, inputs and gradients are zero
-                sum_over_channels<CB>(v, lc);
+                for (int i = 0; i < L; i += 2) {
+                    float v[3][2] = {{d[i % LS], d[(i + 1) % LS]}, {w[i % LS], w[(i + 1) % LS]}, {o[i % LS], o[(i + 1) % LS]}};
+                    if constexpr (NS > 1) {
 #pragma unroll
-                for (int j = 0; j < 16 / CB; ++j) {
-                    const int idx = lc * (16 / CB) + j, i = idx % 8;
-                    if (tk + i < s1) part[((long long)(idx / 8) * g.N + n) * g.ax.ntok + tk + i] = v[j];
+                        for (int k = 0; k < 6; ++k)
+                            v[k / 2][k % 2] = __shfl_sync(0xffffffffu, v[k / 2][k % 2], i / LS * CB + lc);
+                    }
+                    del[i / 2] = pack2(v[0][0], v[0][1]);
+                    dx[i / 2] = pack2(v[1][0], v[1][1]);
+                    go[i / 2] = pack2(v[2][0], v[2][1]);
+                    ddel[i / 2] = du[i / 2] = y[i / 2] = 0;
+                }
+            }
+            __syncwarp();
+            const int at = (n0 + ls) * CB + lc;
+            volatile unsigned long long *win = words_of(warp) + at, *wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
+            const float *pa = sA + at, *ps = start_at(half) + ls * CB + lc;
+            float *psum = sums_of(warp) + at;
+            const ulonglong2 *b4 = reinterpret_cast<const ulonglong2 *>(sB + ls * M::kRow);
+            const ulonglong2 *c4 = reinterpret_cast<const ulonglong2 *>(sC + ls * M::kRow);
+#pragma unroll 1
+            for (int n = ls; n < states + ls; n += NS) {
+                unsigned long long in = *win;
+                const float An = *pa;
+                const f32x2 A22 = dup2(An * kLog2e);
+                float h = live && n < states ? *ps : 0.f;
+                f32x2 a[L / 2], hs[L / 2];       // decays, and the states before the tokens
+                float v[L];
+#pragma unroll
+                for (int q4 = 0; q4 < L / 4; ++q4) {
+                    const ulonglong2 bv = b4[q4], cv = c4[q4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int i = 2 * q4 + k;
+                        float e0, e1, u0, u1;
+                        unpack2(mul2(del[i], A22), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        a[i] = pack2(e0, e1);
+                        unpack2(mul2(dx[i], k ? bv.y : bv.x), u0, u1);
+                        const float h0 = h, h1 = fmaf(e0, h0, u0);
+                        h = fmaf(e1, h1, u1);
+                        hs[i] = pack2(h0, h1);
+                        const f32x2 after = pack2(h1, h);
+                        if (GATE) y[i] = fma2(k ? cv.y : cv.x, after, y[i]);
+                        unpack2(mul2(go[i], after), v[2 * i], v[2 * i + 1]);
+                    }
+                }
+                // dC: lane lc ends with token lc (CB = 16), or tokens 2 lc, 2 lc + 1
+                reduce_halving<CB / 2, 1, L>(v, lane);
+                float *dst = part + ((long long)g.N + n0 + n) * g.ax.ntok + s0 + tile * L + lc * (L / CB);
+#pragma unroll
+                for (int k = 0; k < L / CB; ++k)
+                    if (n < states && lc * (L / CB) + k < have) dst[k] = v[k];
+                // the adjoint behind the tile, once the warp that has the tile behind has left it
+                for (unsigned spin = 0; !__all_sync(0xffffffffu, (unsigned)(in >> 32) == (unsigned)p);) {
+                    in = *win;
+                    if (++spin > kSpinLimit) {
+                        if (lane == 0) atomicOr(g.status, kStatusTimeout);
+                        cp_async_wait();
+                        return;
+                    }
+                }
+                float q = __uint_as_float((unsigned)in);
+                f32x2 dA = 0;
+                const f32x2 An2 = dup2(An);
+#pragma unroll
+                for (int q4 = L / 4 - 1; q4 >= 0; --q4) {
+                    const ulonglong2 bv = b4[q4], cv = c4[q4];
+#pragma unroll
+                    for (int k = 1; k >= 0; --k) {
+                        const int i = 2 * q4 + k;
+                        float c0, c1, e0, e1;
+                        unpack2(mul2(go[i], k ? cv.y : cv.x), c0, c1);
+                        unpack2(a[i], e0, e1);
+                        const float d1 = c1 + q, q1 = e1 * d1;
+                        const float d0 = c0 + q1;
+                        q = e0 * d0;
+                        const f32x2 dh = pack2(d0, d1), m = mul2(pack2(q, q1), hs[i]);   // m: dL/d(delta A)
+                        unpack2(mul2(dh, dx[i]), v[2 * i], v[2 * i + 1]);
+                        du[i] = fma2(dh, k ? bv.y : bv.x, du[i]);
+                        ddel[i] = fma2(m, An2, ddel[i]);
+                        dA = fma2(m, del[i], dA);
+                    }
+                }
+                *wout = (unsigned long long)(unsigned)(p + 1) << 32 | __float_as_uint(q);
+                float a0, a1;
+                unpack2(dA, a0, a1);
+                *psum += a0 + a1;
+                // dB, the same way
+                reduce_halving<CB / 2, 1, L>(v, lane);
+                dst -= (long long)g.N * g.ax.ntok;
+#pragma unroll
+                for (int k = 0; k < L / CB; ++k)
+                    if (n < states && lc * (L / CB) + k < have) dst[k] = v[k];
+                win += NS * CB;
+                wout += NS * CB;
+                pa += NS * CB;
+                ps += NS * CB;
+                psum += NS * CB;
+                b4 += NS * M::kRow / 4;
+                c4 += NS * M::kRow / 4;
+            }
+            if (tile == 0 && g.dstate0 && live) {
+                wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
+                float *o = g.dstate0 + ((long long)u.n * g.D + c) * g.N + n0;
+                for (int n = ls; n < states; n += NS, wout += NS * CB) o[n] = __uint_as_float((unsigned)*wout);
+            }
+            __syncwarp();
+        }
+        // what the rows still hold, before anything is stored
+        float xs[LS], rs[LS], os[LS], zs[LS];
+#pragma unroll
+        for (int i = 0; i < LS; ++i) {
+            const int t = ls * LS + i;
+            xs[i] = to_f(rx[t * CB]);
+            rs[i] = to_f(rx[(L + t) * CB]) + bias;
+            os[i] = to_f(rx[(2 * L + t) * CB]);
+            zs[i] = GATE ? to_f(rx[(3 * L + t) * CB]) : 0.f;
+        }
+        // the states' lanes add up, each keeping its share of the tokens
+        float vu[L], vd[L], vy[L];
+#pragma unroll
+        for (int i = 0; i < L / 2; ++i) {
+            unpack2(du[i], vu[2 * i], vu[2 * i + 1]);
+            unpack2(ddel[i], vd[2 * i], vd[2 * i + 1]);
+            unpack2(y[i], vy[2 * i], vy[2 * i + 1]);
+        }
+        reduce_halving<16, CB, L>(vu, lane);
+        reduce_halving<16, CB, L>(vd, lane);
+        if (GATE) reduce_halving<16, CB, L>(vy, lane);
+        const long long row = (s0 + tile * L + ls * LS) * g.D + c;
+        const int mine_n = live ? have - ls * LS : 0;
+#pragma unroll
+        for (int i = 0; i < LS; i += 2) {
+            float st[2] = {rs[i], rs[i + 1]};
+            if (g.softplus) softplus2(st[0], st[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = i + k;
+                float o = os[j], dz = 0.f;
+                if (GATE) {
+                    const float sg = sigmoid_a(zs[j]), full = fmaf(skip, xs[j], vy[j]);
+                    dz = o * full * sg * fmaf(zs[j], 1.f - sg, 1.f);
+                    o *= zs[j] * sg;
+                }
+                const float dd = fmaf(vu[j], xs[j], vd[j]) * (g.softplus ? sigmoid_a(rs[j]) : 1.f);
+                if (j < mine_n) {
+                    const long long at = row + (long long)j * g.D;
+                    static_cast<T *>(g.dx)[at] = from_f<T>(fmaf(vu[j], st[k], skip * o));
+                    static_cast<T *>(g.ddt)[at] = from_f<T>(dd);
+                    if (GATE) static_cast<T *>(g.dz)[at] = from_f<T>(dz);
+                    sumT += dd;
+                    sumD = fmaf(o, xs[j], sumD);
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            if (!live || tk + i >= s1) continue;
-            const long long t = tk + i;
-            const float r = to_f(dt[t * g.ld_dt]) + bias, xx = to_f(x[t * g.ld_x]);
-            const float dd = (ddel[i] + du[i] * xx) * (g.softplus ? sigmoid_f(r) : 1.f);
-            static_cast<T *>(g.dx)[t * g.D + c] = from_f<T>(fmaf(du[i], del[i], skip * go[i]));
-            static_cast<T *>(g.ddt)[t * g.D + c] = from_f<T>(dd);
-            sumT += dd;
-            sumD = fmaf(go[i], xx, sumD);
-            if (z) {
-                const float zz = to_f(z[t * g.ld_z]), s = sigmoid_f(zz);
-                const float full = fmaf(skip, xx, y[i]);
-                static_cast<T *>(g.dz)[t * g.D + c] =
-                    from_f<T>(to_f(dout[t * g.D]) * full * s * fmaf(zz, 1.f - s, 1.f));
-            }
-        }
+        __syncwarp();
     }
 #pragma unroll
-    for (int o = CB; o < 32; o *= 2) {
+    for (int o = 16; o >= CB; o >>= 1) {
         sumD += __shfl_xor_sync(0xffffffffu, sumD, o);
         sumT += __shfl_xor_sync(0xffffffffu, sumT, o);
     }
-    if (sub == 0) {
-        sA[(warp * (g.N + 2) + g.N) * CB + lc] = sumD;
-        sA[(warp * (g.N + 2) + g.N + 1) * CB + lc] = sumT;
+    if (ls == 0) {
+        sums_of(warp)[padded * CB + lc] = sumD;
+        sums_of(warp)[(padded + 1) * CB + lc] = sumT;
     }
     __syncthreads();
-    float *par_out = g.part_par + (long long)u.n * g.D * (g.N + 2);
-    for (int e = threadIdx.x; e < (g.N + 2) * CB; e += kBwdThreads) {
-        const int n = e % (g.N + 2), j = e / (g.N + 2);
-        const int ch = j < u.live ? u.c0 + j : -1;
-        if (ch < 0) continue;
+    float *out = g.part_par + (long long)u.n * g.D * (g.N + 2);
+    for (int e = warp * 32 + lane; e < (g.N + 2) * CB; e += warps * 32) {
+        const int n = e % (g.N + 2), j = e / (g.N + 2), at = (n < g.N ? n : padded + n - g.N) * CB + j;
+        if (j >= u.live) continue;
         float s = 0.f;
-        for (int w = 0; w < kBwdWarps; ++w) s += sA[(w * (g.N + 2) + n) * CB + j];
-        if (n < g.N) par_out[(long long)ch * g.N + n] = s;
-        else par_out[(long long)g.D * n + ch] = s;
+        for (int w = 0; w < warps; ++w) s += sums_of(w)[at];
+        if (n < g.N) out[(long long)(u.c0 + j) * g.N + n] = s;
+        else out[(long long)g.D * n + u.c0 + j] = s;
     }
-    if (g.dstate0)
-        for (int e = threadIdx.x; e < g.N * CB; e += kBwdThreads) {
-            const int n = e % g.N, j = e / g.N;
-            const int ch = j < u.live ? u.c0 + j : -1;
-            if (ch >= 0) g.dstate0[((long long)u.n * g.D + ch) * g.N + n] = carry[(par * g.N + n) * CB + j];
-        }
 }
 
-// dB, dC of 32 tokens of one group: the tiles' partial sums added in tile order,
-// turned through shared memory into the tensors' layout.
-constexpr int kBcRows = 16;      // (which, state) rows at once
+// dB, dC of 32 tokens of one group: the tiles' partial sums added in tile order and
+// turned through shared memory into the tensors' layout. A warp adds one (which,
+// state) row of the tokens; HBM binds (the partial sums are read once), so the loads of
+// 16 tiles are in flight at a time.
+constexpr int kBcRows = 16;      // (which, state) rows of a CTA, one per warp
 template <typename T>
-__global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmArgs g, int tiles) {
+__global__ void __launch_bounds__(kBcRows * 32) ssm_bc_kernel(const SsmArgs g, int tiles) {
     __shared__ float sm[kBcRows][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = blockIdx.z, r0 = blockIdx.y * kBcRows;
     const long long t0 = (long long)blockIdx.x * 32, t = t0 + lane;
     const long long stride = 2LL * g.N * g.ax.ntok;
-    for (int r0 = 0; r0 < 2 * g.N; r0 += kBcRows) {
-        for (int r = warp; r < kBcRows && r0 + r < 2 * g.N; r += 8) {
-            float s = 0.f;
-            if (t < g.ax.ntok) {
-                const float *p = g.part_bc + (long long)group * tiles * stride + (r0 + r) * g.ax.ntok + t;
-#pragma unroll 8
-                for (int k = 0; k < tiles; ++k) s += p[k * stride];
-            }
-            sm[r][lane] = s;
+    float s = 0.f;
+    if (t < g.ax.ntok && r0 + warp < 2 * g.N) {
+        const float *p = g.part_bc + (long long)group * tiles * stride + (r0 + warp) * g.ax.ntok + t;
+        int k = 0;
+        for (; k + 16 <= tiles; k += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __ldcs(p + (k + i) * stride);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += v[i];
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < 32 * kBcRows; e += 256) {
-            const int r = e % kBcRows, i = e / kBcRows;
-            const int row = r0 + r;
-            if (row >= 2 * g.N || t0 + i >= g.ax.ntok) continue;
-            // tokens of no sequence keep their rows
-            if (g.ax.cu && (t0 + i < g.ax.cu[0] || t0 + i >= g.ax.cu[g.ax.nseq])) continue;
-            T *o = static_cast<T *>(row < g.N ? g.dBm : g.dCm);
-            o[((t0 + i) * g.G + group) * g.N + row % g.N] = from_f<T>(sm[r][i]);
-        }
-        __syncthreads();
+        for (; k < tiles; ++k) s += __ldcs(p + k * stride);
     }
+    sm[warp][lane] = s;
+    __syncthreads();
+    const int r = threadIdx.x % kBcRows, i = threadIdx.x / kBcRows, row = r0 + r;
+    if (row >= 2 * g.N || t0 + i >= g.ax.ntok) return;
+    // tokens of no sequence keep their rows
+    if (g.ax.cu && (t0 + i < g.ax.cu[0] || t0 + i >= g.ax.cu[g.ax.nseq])) return;
+    T *o = static_cast<T *>(row < g.N ? g.dBm : g.dCm);
+    o[((t0 + i) * g.G + group) * g.N + row % g.N] = from_f<T>(sm[r][i]);
 }
 
 // The widest way rows [.][width] at stride ld of several tensors can be copied in
@@ -766,27 +806,37 @@ cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
     const bool wide = 4 * units(16) >= 3LL * sms;
     const long long n = wide ? units(16) : units(8);
     int warps = n <= (wide ? sms : 2 * sms) ? 16 : 8;
-    const long long most = ((g.ax.cu ? g.ax.ntok : g.ax.T) + kFwdL - 1) / kFwdL;
+    const long long most = ((g.ax.cu ? g.ax.ntok : g.ax.T) + kTileL - 1) / kTileL;
     while (warps > 1 && warps / 2 >= most) warps /= 2;
     return wide ? forward_cb<16, OUT, T>(g, n, warps, st) : forward_cb<8, OUT, T>(g, n, warps, st);
 }
 
 constexpr int kBwdCB = 16;
 
-template <typename T>
-cudaError_t backward_t(const SsmArgs &g, cudaStream_t st) {
+template <bool GATE, typename T>
+cudaError_t backward_t(SsmArgs g, int sms, cudaStream_t st) {
     static PerDevice<bool> attr;
+    using M = BwdSmem<kBwdCB, T>;
     const int tiles = ssm_backward_tiles(g.D, g.G);
     const long long units = (long long)g.ax.nseq * tiles;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto kern = ssm_backward_kernel<kBwdCB, T>;
-    cudaError_t e = ensure_smem_attr(attr, kern, (int)BwdSmem<kBwdCB>::bytes(kSsmMaxN));
+    auto kern = ssm_backward_kernel<kBwdCB, GATE, T>;
+    cudaError_t e = ensure_smem_attr(attr, kern, kSmemLimit);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)units, kBwdThreads, BwdSmem<kBwdCB>::bytes(g.N), st>>>(g);
+    // two CTAs of four warps fill an SM's registers (255 of a thread: the tile's six
+    // arrays and a state's decays and walk stand in them; 168 cost spills and 855 us for
+    // 4 x 2048 tokens of 2048 channels against 578); eight warps where CTAs are few
+    int warps = units > 2LL * sms ? 4 : 8;
+    while (warps > 1 && M::bytes(g.N, warps) > (size_t)kSmemLimit) --warps;
+    g.mode_x = copy_mode({{g.x, g.ld_x}, {g.dt, g.ld_dt}, {g.z, g.ld_z}, {g.dout, g.D}}, g.D / g.G, sizeof(T),
+                         kBwdCB * sizeof(T));
+    g.mode_b = copy_mode({{g.Bm, g.ld_b}, {g.Cm, g.ld_c}}, g.N, sizeof(T), 16);
+    g.mode_s = copy_mode({{g.states, g.D}}, g.D / g.G, sizeof(float), 16);
+    kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (g.ax.ntok) {
-        const dim3 grid((unsigned)((g.ax.ntok + 31) / 32), (unsigned)g.G);
-        ssm_bc_kernel<T><<<grid, 256, 0, st>>>(g, tiles / g.G);
+        const dim3 grid((unsigned)((g.ax.ntok + 31) / 32), (unsigned)((2 * g.N + kBcRows - 1) / kBcRows), (unsigned)g.G);
+        ssm_bc_kernel<T><<<grid, kBcRows * 32, 0, st>>>(g, tiles / g.G);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -804,9 +854,11 @@ cudaError_t launch_ssm_forward(const SsmArgs &g, bool bf16, int sms, cudaStream_
 int ssm_backward_tiles(int D, int G) { return G * ((D / G + kBwdCB - 1) / kBwdCB); }
 
 cudaError_t launch_ssm_backward(const SsmArgs &g, bool bf16, int sms, cudaStream_t st) {
-    (void)sms;
     cudaError_t e = cudaSuccess;
-    if (g.ax.nseq) e = bf16 ? backward_t<__nv_bfloat16>(g, st) : backward_t<float>(g, st);
+    if (g.ax.nseq) {
+        if (g.z) e = bf16 ? backward_t<true, __nv_bfloat16>(g, sms, st) : backward_t<true, float>(g, sms, st);
+        else e = bf16 ? backward_t<false, __nv_bfloat16>(g, sms, st) : backward_t<false, float>(g, sms, st);
+    }
     if (e != cudaSuccess) return e;
     const long long da = (long long)g.D * g.N, cols = da + 2LL * g.D;
     return launch_colsum(g.part_par, g.ax.nseq, cols, da, g.dA, g.D, g.dDskip, g.ddt_bias, st);

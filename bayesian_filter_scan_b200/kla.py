@@ -34,7 +34,7 @@ EXPORTS = ("kla_workspace_bytes", "kla_precision_workspace_bytes", "kla_forward"
            "kla_ssm_step", "kla_layernorm_forward", "kla_layernorm_backward_workspace_bytes",
            "kla_layernorm_backward")
 # Tokens between two recorded states, and the most states per channel (include/kla.h kla_ssm_forward)
-SSM_STATE_EVERY, SSM_MAX_STATES = 128, 128
+SSM_STATE_EVERY, SSM_MAX_STATES = 16, 128
 
 
 class KlaError(RuntimeError):

@@ -362,7 +362,7 @@ typedef struct {
  * state0, final_state [Nseq, D, N] fp32; out [Ntok, D] contiguous. z, Dskip,
  * dt_bias, state0 (0), final_state may be NULL. The state is held in fp32.
  * states (or NULL): kla_ssm_states_bytes bytes, 16-byte aligned, receive the
- * state before every 128th token of each sequence for kla_ssm_backward.
+ * state before every 16th token of each sequence for kla_ssm_backward.
  * Preconditions not checked on the device: finite inputs, delta*A <= 0 for a
  * recurrence that stays bounded. N > 128 returns KLA_ERR_UNSUPPORTED. */
 size_t kla_ssm_states_bytes(const kla_ssm_desc *desc);

@@ -65,15 +65,18 @@ def conv(x, w, b, s0, sp, silu=True, dout=None, dfinal=None):
     out, fin = _conv_rows(*leaves, sp, silu)
     pre, _ = _conv_rows(x, w, b, s0, sp, False)
     mag, _ = _conv_rows(x.abs(), w.abs(), b.abs(), s0.abs(), sp, False)
-    # W products and sums, then silu (|silu'| <= 1.1; its value within 10 U of itself)
-    res = {"out": (out.detach(), (W + 1) * U * 1.1 * mag + (12 * U * pre.abs() if silu else 0)), "final": (fin.detach(), 0.0)}
+    # W products and sums, then silu (|silu'| <= 1.1). Its value: a power of two within 4 U whose
+    # exponent's product is off by |pre| log2(e) U, hence itself by |pre| U; sum, quotient, product 4 U
+    act = (12 + pre.abs()) * U
+    res = {"out": (out.detach(), (W + 1) * U * 1.1 * mag + (act * pre.abs() if silu else 0)), "final": (fin.detach(), 0.0)}
     if dout is None:
         return res
     rows = torch.cat([dout[a:e] for a, e in sp]).double()
     dfin = torch.zeros_like(fin) if dfinal is None else dfinal.double()
     gx, gw, gb, gs = torch.autograd.grad([out, fin], leaves, [rows, dfin], materialize_grads=True)
     tok = torch.cat([torch.arange(a, e) for a, e in sp])
-    # d = dout silu'(pre): |silu''| <= 0.5 carries pre's error; the slope's own within 20 U
+    # d = dout silu'(pre): |silu''| <= 0.5 carries pre's error; the slope s (1 + pre (1 - s)) with s
+    # within (8 + |pre|) U and s (1 - s) <= 1/4: within 20 U (1 + |pre|)
     s = torch.sigmoid(pre)
     slope = s * (1 + pre * (1 - s)) if silu else torch.ones_like(pre)
     derr = rows.abs() * ((0.5 * (W + 1) * U * mag + 20 * U * (1 + pre.abs())) if silu else 0 * mag)

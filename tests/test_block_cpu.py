@@ -141,18 +141,18 @@ def test_null_descriptors(L):
 
 
 def test_state_records_cover_every_sequence():
-    # record k of sequence n sits at s0 // 128 + n + k: no two sequences share one
+    # record k of sequence n sits at s0 // 16 + n + k: no two sequences share one
     g = torch.Generator().manual_seed(0)
     for _ in range(200):
         lens = torch.randint(0, 400, (int(torch.randint(1, 9, (1,), generator=g)),), generator=g).tolist()
         used, s0 = set(), 0
         for n, m in enumerate(lens):
-            for k in range(-(-m // 128)):
-                i = s0 // 128 + n + k
+            for k in range(-(-m // 16)):
+                i = s0 // 16 + n + k
                 assert i not in used
                 used.add(i)
             s0 += m
-        assert not used or max(used) < s0 // 128 + len(lens) + 1
+        assert not used or max(used) < s0 // 16 + len(lens) + 1
 
 
 def test_cpu_tensors_are_refused(L):
