@@ -381,7 +381,7 @@ kla_status kla_ssm_step(const kla_ssm_desc *d, const void *x, const void *dt, co
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     g.final_state = state;
     g.out = out;
-    return of_cuda(launch_ssm_step(g, d->dtype == KLA_BF16, st));
+    return of_cuda(launch_ssm_step(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
 kla_status kla_layernorm_forward(const kla_norm_desc *d, const void *x, const void *residual, const float *weight,

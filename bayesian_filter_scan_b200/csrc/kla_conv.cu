@@ -38,12 +38,20 @@ template <int W, int V>
 struct Taps {
     float w[W][V], b[V];
     __device__ __forceinline__ void load(const ConvArgs &g, int c) {
+        if (W == 4 && ((uintptr_t)g.w & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < V; ++i) {
+                const float4 t = __ldg(reinterpret_cast<const float4 *>(g.w) + c + i);
+                w[0][i] = t.x; w[1 % W][i] = t.y; w[2 % W][i] = t.z; w[3 % W][i] = t.w;
+            }
+        } else {
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = __ldg(g.w + (c + i) * W + k);
-            b[i] = g.bias ? __ldg(g.bias + c + i) : 0.f;
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int k = 0; k < W; ++k) w[k][i] = __ldg(g.w + (c + i) * W + k);
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) b[i] = g.bias ? __ldg(g.bias + c + i) : 0.f;
     }
 };
 
@@ -337,30 +345,45 @@ __global__ void __launch_bounds__(kConvThreads) conv_dstate_kernel(const ConvArg
     }
 }
 
-// One token per row: the state's rows move down by one, x becomes the last.
+// One token per row: the state's rows move down by one, x becomes the last. A thread
+// takes the same channels of `run` rows, for which it loads the taps once.
 template <int W, int V, typename T>
-__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvArgs g, int nvec) {
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const ConvArgs g, int nvec, int run) {
     const long long e = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-    const long long n = e / nvec;
-    if (n >= g.ax.nseq) return;
-    const int c = (int)(e - n * nvec) * V;
-    T *state = static_cast<T *>(g.final_state) + n * (W - 1) * g.D + c;
-    float win[W][V], y[V];
+    long long n = e / nvec * run;
+    const long long end = min(n + run, (long long)g.ax.nseq);
+    if (n >= end) return;
+    const int c = (int)(e % nvec) * V;
+    Raw<V, T> in[W], next[W];
+    auto load = [&](Raw<V, T>(&r)[W], long long row) {
+        const T *state = static_cast<const T *>(g.final_state) + row * (W - 1) * g.D + c;
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) load_v<V>(state + (long long)r * g.D, win[r]);
-    load_v<V>(static_cast<const T *>(g.x) + n * g.ld_x + c, win[W - 1]);
+        for (int i = 0; i < W - 1; ++i) r[i].load(state + (long long)i * g.D);
+        r[W - 1].load(static_cast<const T *>(g.x) + row * g.ld_x + c);
+    };
+    load(in, n);
     Taps<W, V> k;
     k.load(g, c);
+    for (; n < end; ++n) {
+        if (n + 1 < end) load(next, n + 1);
+        float a[V], f[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float a = k.b[i];
+        for (int i = 0; i < V; ++i) a[i] = k.b[i];
+        T *state = static_cast<T *>(g.final_state) + n * (W - 1) * g.D + c;
 #pragma unroll
-        for (int r = 0; r < W; ++r) a = fmaf(k.w[r][i], win[r][i], a);
-        y[i] = g.silu ? a * sigmoid_for<T>(a) : a;
+        for (int r = 0; r < W; ++r) {
+            in[r].get(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] = fmaf(k.w[r][i], f[i], a[i]);
+            if (r) store_v<V>(state + (long long)(r - 1) * g.D, f);
+        }
+        if (g.silu)
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] *= sigmoid_for<T>(a[i]);
+        store_v<V>(static_cast<T *>(g.out) + n * g.D + c, a);
+#pragma unroll
+        for (int r = 0; r < W; ++r) in[r] = next[r];
     }
-    store_v<V>(static_cast<T *>(g.out) + n * g.D + c, y);
-#pragma unroll
-    for (int r = 0; r < W - 1; ++r) store_v<V>(state + (long long)r * g.D, win[r + 1]);
 }
 
 bool al(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -410,10 +433,12 @@ cudaError_t backward_t(const ConvArgs &g, cudaStream_t st) {
 template <int W, int V, typename T>
 cudaError_t step_t(const ConvArgs &g, cudaStream_t st) {
     const int nvec = (g.D + V - 1) / V;
-    const long long n = (long long)nvec * g.ax.nseq, blocks = (n + kConvThreads - 1) / kConvThreads;
+    int run = 8;
+    while (run > 1 && (long long)nvec * (g.ax.nseq / run) < 148LL * 256) run /= 2;
+    const long long n = (long long)nvec * ((g.ax.nseq + run - 1) / run), blocks = (n + kConvThreads - 1) / kConvThreads;
     if (!blocks) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    conv_step_kernel<W, V, T><<<(unsigned)blocks, kConvThreads, 0, st>>>(g, nvec);
+    conv_step_kernel<W, V, T><<<(unsigned)blocks, kConvThreads, 0, st>>>(g, nvec, run);
     return cudaGetLastError();
 }
 
@@ -422,11 +447,11 @@ enum class Call { kForward, kBackward, kStep };
 template <int W, typename T>
 cudaError_t conv_w(const ConvArgs &g, Call call, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
-    const bool vec = rows_aligned(g, sizeof(T), call == Call::kStep ? 16 : 8);
+    const bool vec = rows_aligned(g, sizeof(T), 8);
     // 8-byte accesses, four rows ahead: 80 registers (32768 tokens of 2048 channels 70 us;
     // 78 eight rows ahead, 85 and 93 with 16-byte accesses, whose registers halve the warps)
     if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, st) : forward_t<W, 1, 8, T>(g, st);
-    if (call == Call::kStep) return vec ? step_t<W, V, T>(g, st) : step_t<W, 1, T>(g, st);
+    if (call == Call::kStep) return vec ? step_t<W, V / 2, T>(g, st) : step_t<W, 1, T>(g, st);
     // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers
     return vec ? backward_t<W, V / 2, T>(g, st) : backward_t<W, 1, T>(g, st);
 }

@@ -32,40 +32,7 @@ namespace {
 constexpr int kTileL = 16;       // tokens of a tile
 constexpr int kTileNB = 16;      // states whose B and C a warp stages at once
 constexpr int kLdPad = 4;        // floats behind a state's tokens in shared memory: states on other banks
-constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// softplus(x) = max(x, 0) + log(1 + y) of two values, y = e^-|x| in (0, 1]. log(1 + y)
-// is y times a polynomial of degree 9 fitted to log(1 + y) / y on [0, 1] for the least
-// relative error (5e-9; 1.5e-7 with fp32's rounding), so a small y keeps its digits,
-// which the logarithm of a rounded 1 + y would not.
-__device__ __forceinline__ void softplus2(float &x0, float &x1) {
-    const f32x2 y = pack2(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
-    f32x2 p = dup2(-0.0032439809f);
-    p = fma2(p, y, dup2(0.019851264f));
-    p = fma2(p, y, dup2(-0.05695916f));
-    p = fma2(p, y, dup2(0.10603617f));
-    p = fma2(p, y, dup2(-0.1530557f));
-    p = fma2(p, y, dup2(0.19675931f));
-    p = fma2(p, y, dup2(-0.24954133f));
-    p = fma2(p, y, dup2(0.33329964f));
-    p = fma2(p, y, dup2(-0.499999f));
-    p = fma2(p, y, dup2(1.f));
-    float m0, m1;
-    unpack2(fma2(p, y, pack2(fmaxf(x0, 0.f), fmaxf(x1, 0.f))), m0, m1);
-    x0 = m0;
-    x1 = m1;
-}
 __device__ __forceinline__ float sigmoid_a(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 // How rows reach shared memory: pieces of 16 bytes (or a whole narrower row), of 4

@@ -1,7 +1,8 @@
 // kla_ssm_step.cu -- one token per row through the selective scan, the state
 // updated in place (sm_100a). Per channel N states are read and written in fp32
 // (8 N bytes) for a handful of operations: HBM binds for many rows, launch
-// latency for few.
+// latency for few. `lanes` lanes (a power of two) share a channel of a row; a
+// thread walks rows with the next one's reads on their way while it works on this one.
 #include "kla_block.cuh"
 
 namespace kla {
@@ -9,64 +10,121 @@ namespace kla {
 namespace {
 
 constexpr int kStepThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-
-// `lanes` lanes (a power of two) share a channel; each takes V states at a time.
+// What one lane reads of a row: V states, and its scalars.
 template <int V, typename T>
-__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs g, int lanes, long long items) {
-    const long long e = ((long long)blockIdx.x * kStepThreads + threadIdx.x) / lanes;
-    const int l = threadIdx.x % lanes;
-    const bool live = e < items;
-    const long long row = live ? e / g.D : 0;
-    const int c = live ? (int)(e - row * g.D) : 0, group = c / (g.D / g.G);
-    const float x = to_f(static_cast<const T *>(g.x)[row * g.ld_x + c]);
-    const float r = to_f(static_cast<const T *>(g.dt)[row * g.ld_dt + c]) + (g.dt_bias ? g.dt_bias[c] : 0.f);
-    const float del = g.softplus ? softplus_f(r) : r, dx = del * x;
-    const T *Bm = static_cast<const T *>(g.Bm) + row * g.ld_b + (long long)group * g.N;
-    const T *Cm = static_cast<const T *>(g.Cm) + row * g.ld_c + (long long)group * g.N;
-    const float *A = g.A + (long long)c * g.N;
-    float *state = g.final_state + (row * g.D + c) * g.N;
-    float y = 0.f;
-    for (int n = l * V; n < g.N; n += lanes * V) {
-        float h[V], a[V];
-        load_v<V>(state + n, h);
-        load_v<V>(A + n, a);
+struct StepRow {
+    Raw<V, float> h;
+    Raw<V, T> b, c;
+    T x, dt, z;
+};
+
+// Grid: channels x row groups; a thread keeps its channel, whose A it holds, and walks
+// rows. V states at a time: 4 (rows of A and the state on 16-byte boundaries, of B and C
+// on as many elements' when vec_bc) with all N states in one round of the lanes, or 1.
+template <int V, typename T>
+__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs g, int lanes, bool vec_bc) {
+    const int l = threadIdx.x % lanes, rows = g.ax.nseq;
+    const int at = (int)(((long long)blockIdx.x * kStepThreads + threadIdx.x) / lanes);
+    const bool live = at < g.D;        // the others keep their warp's shuffles company
+    const int c = live ? at : 0, group = c / (g.D / g.G);
+    auto load = [&](StepRow<V, T> &it, long long row, int n) {
+        it.x = static_cast<const T *>(g.x)[row * g.ld_x + c];
+        it.dt = static_cast<const T *>(g.dt)[row * g.ld_dt + c];
+        if (g.z) it.z = static_cast<const T *>(g.z)[row * g.ld_z + c];
+        if (n >= g.N) return;
+        it.h.load(g.final_state + (row * g.D + c) * g.N + n);
+        const T *B = static_cast<const T *>(g.Bm) + row * g.ld_b + (long long)group * g.N + n;
+        const T *C = static_cast<const T *>(g.Cm) + row * g.ld_c + (long long)group * g.N + n;
+        if (V == 1 || vec_bc) {
+            it.b.load(B);
+            it.c.load(C);
+        } else {
+            float f[V], k[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            h[i] = fmaf(exp2f(del * (a[i] * kLog2e)), h[i], dx * to_f(Bm[n + i]));
-            y = fmaf(to_f(Cm[n + i]), h[i], y);
+            for (int i = 0; i < V; ++i) f[i] = to_f(B[i]), k[i] = to_f(C[i]);
+            it.b.set(f);
+            it.c.set(k);
         }
-        if (live) store_v<V>(state + n, h);
+    };
+    StepRow<V, T> cur, next;
+    int row = blockIdx.y;
+    if (live) load(cur, row, l * V);
+    const float bias = g.dt_bias ? g.dt_bias[c] : 0.f, skip = g.Dskip ? g.Dskip[c] : 0.f;
+    float a[V];
+    auto load_a = [&](int n) {
+        load_v<V>(g.A + (long long)c * g.N + n, a);
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] *= kLog2e;
+    };
+    if (l * V < g.N) load_a(l * V);
+    for (; row < rows; row += gridDim.y) {
+        if (live && row + gridDim.y < rows) load(next, row + gridDim.y, l * V);
+        float y = 0.f;
+        if (live) {
+            float del = to_f(cur.dt) + bias, spare = 0.f;
+            if (g.softplus) softplus2(del, spare);
+            const float dx = del * to_f(cur.x);
+            for (int n = l * V; n < g.N; n += lanes * V) {
+                if (lanes * V < g.N) {
+                    load(cur, row, n);
+                    load_a(n);
+                }
+                float h[V], b[V], cc[V];
+                cur.h.get(h);
+                cur.b.get(b);
+                cur.c.get(cc);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    h[i] = fmaf(ex2(del * a[i]), h[i], dx * b[i]);
+                    y = fmaf(cc[i], h[i], y);
+                }
+                store_v<V>(g.final_state + ((long long)row * g.D + c) * g.N + n, h);
+            }
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (live && l == 0) {
+            float v = fmaf(skip, to_f(cur.x), y);
+            if (g.z) {
+                const float z = to_f(cur.z);
+                v *= z * sigmoid_for<T>(z);
+            }
+            static_cast<T *>(g.out)[(long long)row * g.D + c] = from_f<T>(v);
+        }
+        cur = next;
     }
-    for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (!live || l) return;
-    if (g.Dskip) y = fmaf(g.Dskip[c], x, y);
-    if (g.z) {
-        const float zz = to_f(static_cast<const T *>(g.z)[row * g.ld_z + c]);
-        y *= zz * sigmoid_f(zz);
-    }
-    static_cast<T *>(g.out)[row * g.D + c] = from_f<T>(y);
 }
 
 template <int V, typename T>
-cudaError_t step_t(const SsmArgs &g, cudaStream_t st) {
+cudaError_t step_t(const SsmArgs &g, bool vec_bc, int sms, cudaStream_t st) {
     int lanes = 1;
-    while (lanes < 8 && lanes * V < g.N) lanes *= 2;
-    const long long items = (long long)g.ax.nseq * g.D, blocks = (items * lanes + kStepThreads - 1) / kStepThreads;
-    if (!blocks) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    ssm_step_kernel<V, T><<<(unsigned)blocks, kStepThreads, 0, st>>>(g, lanes, items);
+    while (lanes < 32 && lanes * V < g.N) lanes *= 2;
+    const unsigned bx = (unsigned)(((long long)g.D * lanes + kStepThreads - 1) / kStepThreads);
+    const int rows = g.ax.nseq;
+    if (!rows) return cudaSuccess;
+    long long by = (8LL * sms + bx - 1) / bx;
+    if (by > rows) by = rows;
+    if (by > 65535) by = 65535;
+    // as many rows for every group, as far as they go
+    by = (rows + (rows + by - 1) / by - 1) / ((rows + by - 1) / by);
+    ssm_step_kernel<V, T><<<dim3(bx, (unsigned)by), kStepThreads, 0, st>>>(g, lanes, vec_bc);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t step_any(const SsmArgs &g, int sms, cudaStream_t st) {
+    auto al = [](const void *p, long long bytes, size_t a) { return (((uintptr_t)p | (size_t)bytes) & (a - 1)) == 0; };
+    constexpr size_t four = 4 * sizeof(T);
+    const long long es = sizeof(T);
+    const bool vec = g.N % 4 == 0 && al(g.A, 0, 16) && al(g.final_state, 0, 16);
+    const bool vec_bc = vec && al(g.Bm, g.ld_b * es, four) && al(g.Cm, g.ld_c * es, four);
+    return vec ? step_t<4, T>(g, vec_bc, sms, st) : step_t<1, T>(g, true, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_ssm_step(const SsmArgs &g, bool bf16, cudaStream_t st) {
-    const bool vec = g.N % 4 == 0 && ((uintptr_t)g.A & 15) == 0 && ((uintptr_t)g.final_state & 15) == 0;
-    if (bf16) return vec ? step_t<4, __nv_bfloat16>(g, st) : step_t<1, __nv_bfloat16>(g, st);
-    return vec ? step_t<4, float>(g, st) : step_t<1, float>(g, st);
+cudaError_t launch_ssm_step(const SsmArgs &g, bool bf16, int sms, cudaStream_t st) {
+    return bf16 ? step_any<__nv_bfloat16>(g, sms, st) : step_any<float>(g, sms, st);
 }
 
 }  // namespace kla

@@ -384,62 +384,74 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-class _on:
-    """The device of a call's tensors made current while the call enqueues its
-    work; the work goes on that device's current stream."""
-    __slots__ = ("ctx",)
+# the current stream's handle on a device, without the object around it where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device):
-        self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+def _enqueue(fn, x, *args):
+    """Calls the library for tensors on x's device: that device made current, the work
+    on its current stream."""
+    index = x.get_device()
+    if index == torch.cuda.current_device():
+        s = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            s = fn(*args, _raw_stream(index))
+    if s != KLA_OK:
+        raise KlaError(s, fn.__name__)
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _bytes(fn, x, *args):
+    """A size that the library computes for x's device."""
+    if x.get_device() == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(x.get_device()):
+        return fn(*args)
 
 
 def _io_dtype(x):
     if not x.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if x.dtype not in _DTYPES:
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
         raise TypeError("token tensors must be bfloat16 or float32")
-    return _DTYPES[x.dtype]
+    return dt
 
 
 def _tokens(name, t, like, shape):
     """A token tensor: like's dtype and device, the given shape, rows at one
-    stride with contiguous values. Returns the token stride."""
-    if t.dtype != like.dtype:
+    stride with contiguous values. Returns the token stride, or 0 for a
+    contiguous tensor."""
+    if t.dtype is not like.dtype:
         raise TypeError("%s must have the dtype of x" % name)
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError("%s must be on the device of x" % name)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
-    width = 1
-    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and st != width:
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.is_contiguous():
+        return 0
+    st, width = t.stride(), 1
+    for n, k in zip(reversed(shape[1:]), reversed(st[1:])):
+        if n > 1 and k != width:
             raise ValueError("the values of a row of %s must be contiguous" % name)
         width *= n
     if shape[0] <= 1:
-        return width
-    if t.stride(0) < width:
+        return 0
+    if st[0] < width:
         raise ValueError("rows of %s must not overlap" % name)
-    return t.stride(0)
+    return st[0]
 
 
 def _dense(name, t, like, shape, dtype=_F32):
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError("%s must be on the device of x" % name)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with shape %s" % (name, shape))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape %s" % (name, tuple(shape)))
 
 
 def _axis(x, cu_seqlens, B, T):
@@ -456,7 +468,8 @@ def _axis(x, cu_seqlens, B, T):
         return 1, n, cu_seqlens.data_ptr(), k, k
     if B is None:
         B = 1 if T is None else (n // T if T else 0)
-    T = T if T is not None else (n // B if B else 0)
+    if T is None:
+        T = n // B if B else 0
     if B < 0 or T < 0 or B * T != n:
         raise ValueError("B*T must equal the number of tokens")
     return B, T, None, 0, B
@@ -464,7 +477,7 @@ def _axis(x, cu_seqlens, B, T):
 
 def _out_like(name, out, x, shape):
     if out is None:
-        return torch.empty(shape, dtype=x.dtype, device=x.device)
+        return x.new_empty(shape)
     _dense(name, out, x, shape, x.dtype)
     return out
 
@@ -476,7 +489,7 @@ def _conv(x, weight, bias, cu_seqlens, B, T, silu):
     D, W = x.shape[1], weight.shape[1]
     if not 1 <= W <= 4:
         raise ValueError("a convolution has 1 to 4 taps")
-    ld = _tokens("x", x, x, tuple(x.shape))
+    ld = _tokens("x", x, x, x.shape)
     _dense("weight", weight, x, (D, W))
     _dense("bias", bias, x, (D,))
     b, t, cu, k, N = _axis(x, cu_seqlens, B, T)
@@ -491,11 +504,9 @@ def conv_forward(x, weight, bias=None, state0=None, cu_seqlens=None, B=None, T=N
     ``(out, state)`` with ``final_state``: the history after each sequence."""
     d, D, W, N = _conv(x, weight, bias, cu_seqlens, B, T, silu)
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
-    with _on(x.device) as stream:
-        out = _out_like("out", out, x, (x.shape[0], D))
-        fs = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device) if final_state else None
-        s = lib().kla_conv_forward(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(out), _p(fs), stream)
-    _check(s, "kla_conv_forward")
+    out = _out_like("out", out, x, (x.shape[0], D))
+    fs = x.new_empty((N, W - 1, D)) if final_state else None
+    _enqueue(lib().kla_conv_forward, x, ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(out), _p(fs))
     return (out, fs) if final_state else out
 
 
@@ -508,18 +519,16 @@ def conv_backward(x, weight, dout, bias=None, state0=None, dfinal_state=None, cu
     _dense("dout", dout, x, (x.shape[0], D), x.dtype)
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
     _dense("dfinal_state", dfinal_state, x, (N, W - 1, D), x.dtype)
-    with _on(x.device) as stream:
-        io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
-        g = {"dx": torch.empty((x.shape[0], D), **io), "dweight": torch.empty((D, W), **f32),
-             "dbias": torch.empty(D, **f32)}
-        if state0 is not None:
-            g["dstate0"] = torch.empty((N, W - 1, D), **io)
-        need = lib().kla_conv_backward_workspace_bytes(ctypes.byref(d))
-        workspace = _workspace(workspace, need, x)
-        s = lib().kla_conv_backward(ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(dout),
-                                    _p(dfinal_state), _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]),
-                                    _p(g.get("dstate0")), _p(workspace), workspace.numel(), stream)
-    _check(s, "kla_conv_backward")
+    io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
+    g = {"dx": torch.empty((x.shape[0], D), **io), "dweight": torch.empty((D, W), **f32),
+         "dbias": torch.empty(D, **f32)}
+    if state0 is not None:
+        g["dstate0"] = torch.empty((N, W - 1, D), **io)
+    need = _bytes(lib().kla_conv_backward_workspace_bytes, x, ctypes.byref(d))
+    workspace = _workspace(workspace, need, x)
+    _enqueue(lib().kla_conv_backward, x, ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(dout),
+             _p(dfinal_state), _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]),
+             _p(g.get("dstate0")), _p(workspace), workspace.numel())
     return g
 
 
@@ -536,11 +545,9 @@ def conv_step(x, weight, state, bias=None, silu=True, out=None):
     Returns out [B, D]."""
     d, D, W, N = _conv(x, weight, bias, None, x.shape[0], 1, silu)
     _dense("state", state, x, (N, W - 1, D), x.dtype)
-    with _on(x.device) as stream:
-        out = _out_like("out", out, x, (N, D))
-        s = lib().kla_conv_step(ctypes.byref(d), x.data_ptr(), weight.data_ptr(), _p(bias), _p(state),
-                                out.data_ptr(), stream)
-    _check(s, "kla_conv_step")
+    out = _out_like("out", out, x, (N, D))
+    _enqueue(lib().kla_conv_step, x, ctypes.byref(d), x.data_ptr(), weight.data_ptr(), _p(bias), _p(state),
+             out.data_ptr())
     return out
 
 
@@ -552,8 +559,9 @@ def _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus):
     G, N = Bm.shape[1], A.shape[1]
     if G < 1 or ch % G:
         raise ValueError("the groups of Bm must divide the channels")
-    ld = (_tokens("x", x, x, (n, ch)), _tokens("dt", dt, x, (n, ch)),
-          _tokens("z", z, x, (n, ch)) if z is not None else 0,
+    shape = x.shape
+    ld = (_tokens("x", x, x, shape), _tokens("dt", dt, x, shape),
+          _tokens("z", z, x, shape) if z is not None else 0,
           _tokens("Bm", Bm, x, (n, G, N)), _tokens("Cm", Cm, x, (n, G, N)))
     _dense("A", A, x, (ch, N))
     _dense("D", D, x, (ch,))
@@ -571,15 +579,13 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state0=None, cu_
     ``save_states``."""
     d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
     _dense("state0", state0, x, (seqs, ch, N))
-    with _on(x.device) as stream:
-        out = _out_like("out", out, x, (x.shape[0], ch))
-        fs = torch.empty((seqs, ch, N), dtype=_F32, device=x.device) if final_state else None
-        st = None
-        if save_states:
-            st = torch.empty(lib().kla_ssm_states_bytes(ctypes.byref(d)) // 4, dtype=_F32, device=x.device)
-        s = lib().kla_ssm_forward(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
-                                  _p(state0), _p(out), _p(fs), _p(st), stream)
-    _check(s, "kla_ssm_forward")
+    out = _out_like("out", out, x, (x.shape[0], ch))
+    fs = torch.empty((seqs, ch, N), dtype=_F32, device=x.device) if final_state else None
+    st = None
+    if save_states:
+        st = torch.empty(lib().kla_ssm_states_bytes(ctypes.byref(d)) // 4, dtype=_F32, device=x.device)
+    _enqueue(lib().kla_ssm_forward, x, ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
+             _p(state0), _p(out), _p(fs), _p(st))
     res = (out,) + ((fs,) if final_state else ()) + ((st,) if save_states else ())
     return res if len(res) > 1 else out
 
@@ -598,20 +604,18 @@ def ssm_backward(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, state0=No
     L = lib()
     if states is not None:
         _dense("states", states, x, (L.kla_ssm_states_bytes(ctypes.byref(d)) // 4,))
-    with _on(x.device) as stream:
-        io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
-        g = {"dx": torch.empty((n, ch), **io), "ddt": torch.empty((n, ch), **io),
-             "dBm": torch.empty((n, G, N), **io), "dCm": torch.empty((n, G, N), **io),
-             "dA": torch.empty((ch, N), **f32), "dD": torch.empty(ch, **f32), "ddt_bias": torch.empty(ch, **f32),
-             "dstate0": torch.empty((seqs, ch, N), **f32)}
-        if z is not None:
-            g["dz"] = torch.empty((n, ch), **io)
-        workspace = _workspace(workspace, L.kla_ssm_backward_workspace_bytes(ctypes.byref(d), states is not None), x)
-        s = L.kla_ssm_backward(ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
-                               _p(state0), _p(states), _p(dout), _p(dfinal_state), _p(g["dx"]), _p(g["ddt"]),
-                               _p(g["dA"]), _p(g["dBm"]), _p(g["dCm"]), _p(g["dD"]), _p(g.get("dz")),
-                               _p(g["ddt_bias"]), _p(g["dstate0"]), _p(workspace), workspace.numel(), stream)
-    _check(s, "kla_ssm_backward")
+    io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
+    g = {"dx": torch.empty((n, ch), **io), "ddt": torch.empty((n, ch), **io),
+         "dBm": torch.empty((n, G, N), **io), "dCm": torch.empty((n, G, N), **io),
+         "dA": torch.empty((ch, N), **f32), "dD": torch.empty(ch, **f32), "ddt_bias": torch.empty(ch, **f32),
+         "dstate0": torch.empty((seqs, ch, N), **f32)}
+    if z is not None:
+        g["dz"] = torch.empty((n, ch), **io)
+    workspace = _workspace(workspace, _bytes(L.kla_ssm_backward_workspace_bytes, x, ctypes.byref(d), states is not None), x)
+    _enqueue(L.kla_ssm_backward, x, ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
+             _p(state0), _p(states), _p(dout), _p(dfinal_state), _p(g["dx"]), _p(g["ddt"]),
+             _p(g["dA"]), _p(g["dBm"]), _p(g["dCm"]), _p(g["dD"]), _p(g.get("dz")),
+             _p(g["ddt_bias"]), _p(g["dstate0"]), _p(workspace), workspace.numel())
     return g
 
 
@@ -620,11 +624,9 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, softplus=Tru
     ``state`` [B, D, N] is updated in place. Returns out [B, D]."""
     d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, None, x.shape[0], 1, softplus)
     _dense("state", state, x, (seqs, ch, N))
-    with _on(x.device) as stream:
-        out = _out_like("out", out, x, (seqs, ch))
-        s = lib().kla_ssm_step(ctypes.byref(d), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
-                               Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), state.data_ptr(), out.data_ptr(), stream)
-    _check(s, "kla_ssm_step")
+    out = _out_like("out", out, x, (seqs, ch))
+    _enqueue(lib().kla_ssm_step, x, ctypes.byref(d), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+             Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), state.data_ptr(), out.data_ptr())
     return out
 
 
@@ -632,7 +634,7 @@ def _norm(x, weight, bias, residual, eps):
     dt = _io_dtype(x)
     if x.dim() != 2 or x.shape[1] < 1:
         raise ValueError("x must be [rows, D]")
-    shape = tuple(x.shape)
+    shape = x.shape
     ld = _tokens("x", x, x, shape)
     ld_r = _tokens("residual", residual, x, shape) if residual is not None else 0
     _dense("weight", weight, x, shape[1:])
@@ -647,16 +649,14 @@ def layernorm_forward(x, weight=None, bias=None, residual=None, eps=1e-5, stats=
     d, shape = _norm(x, weight, bias, residual, eps)
     if sum_out is not None and residual is None:
         raise ValueError("sum_out goes with a residual")
-    with _on(x.device) as stream:
-        out = _out_like("out", out, x, shape)
-        total = _out_like("sum_out", sum_out, x, shape) if residual is not None else None
-        mean = rstd = None
-        if stats:
-            mean = torch.empty(shape[0], dtype=_F32, device=x.device)
-            rstd = torch.empty(shape[0], dtype=_F32, device=x.device)
-        s = lib().kla_layernorm_forward(ctypes.byref(d), _p(x), _p(residual), _p(weight), _p(bias), _p(out),
-                                        _p(total), _p(mean), _p(rstd), stream)
-    _check(s, "kla_layernorm_forward")
+    out = _out_like("out", out, x, shape)
+    total = _out_like("sum_out", sum_out, x, shape) if residual is not None else None
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(shape[0], dtype=_F32, device=x.device)
+        rstd = torch.empty(shape[0], dtype=_F32, device=x.device)
+    _enqueue(lib().kla_layernorm_forward, x, ctypes.byref(d), _p(x), _p(residual), _p(weight), _p(bias), _p(out),
+             _p(total), _p(mean), _p(rstd))
     res = (out,) + ((total,) if residual is not None else ()) + ((mean, rstd) if stats else ())
     return res if len(res) > 1 else out
 
@@ -671,15 +671,13 @@ def layernorm_backward(x, dout, mean, rstd, weight=None, dsum=None, workspace=No
     _dense("rstd", rstd, x, shape[:1])
     _dense("dout", dout, x, shape, x.dtype)
     _dense("dsum", dsum, x, shape, x.dtype)
-    with _on(x.device) as stream:
-        f32 = dict(dtype=_F32, device=x.device)
-        g = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device), "dweight": torch.empty(shape[1], **f32),
-             "dbias": torch.empty(shape[1], **f32)}
-        workspace = _workspace(workspace, lib().kla_layernorm_backward_workspace_bytes(ctypes.byref(d)), x)
-        s = lib().kla_layernorm_backward(ctypes.byref(d), _p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dsum),
-                                         _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]), _p(workspace),
-                                         workspace.numel(), stream)
-    _check(s, "kla_layernorm_backward")
+    f32 = dict(dtype=_F32, device=x.device)
+    g = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device), "dweight": torch.empty(shape[1], **f32),
+         "dbias": torch.empty(shape[1], **f32)}
+    workspace = _workspace(workspace, _bytes(lib().kla_layernorm_backward_workspace_bytes, x, ctypes.byref(d)), x)
+    _enqueue(lib().kla_layernorm_backward, x, ctypes.byref(d), _p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dsum),
+             _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]), _p(workspace),
+             workspace.numel())
     return g
 
 
