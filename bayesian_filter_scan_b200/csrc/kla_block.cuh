@@ -295,7 +295,7 @@ struct SsmArgs {
     float *part_par;   // [nseq][D*N of dA, then D of dDskip, then D of ddt_bias]
 };
 cudaError_t launch_ssm_forward(const SsmArgs &, bool bf16, int sms, cudaStream_t);
-int ssm_backward_tiles(int D, int G);
+int ssm_backward_tiles(int D, int G, int nseq, int sms);
 cudaError_t launch_ssm_backward(const SsmArgs &, bool bf16, int sms, cudaStream_t);
 cudaError_t launch_ssm_step(const SsmArgs &, bool bf16, int sms, cudaStream_t);
 

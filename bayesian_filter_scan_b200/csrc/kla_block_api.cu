@@ -154,7 +154,7 @@ struct SsmWorkspace { size_t bc, par, states, total; };
 SsmWorkspace ssm_workspace(const SsmArgs &g, bool with_states) {
     SsmWorkspace w;
     w.bc = 0;
-    w.par = align256((size_t)ssm_backward_tiles(g.D, g.G) * 2 * g.N * g.ax.ntok * sizeof(float));
+    w.par = align256((size_t)ssm_backward_tiles(g.D, g.G, g.ax.nseq, sm_count()) * 2 * g.N * g.ax.ntok * sizeof(float));
     w.states = w.par + align256((size_t)g.ax.nseq * g.D * (g.N + 2) * sizeof(float));
     w.total = w.states + (with_states ? 0 : align256(ssm_state_records(g)));
     return w;

@@ -772,22 +772,21 @@ cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
     // 600, 586 and 671 us.
     const bool wide = 4 * units(16) >= 3LL * sms;
     const long long n = wide ? units(16) : units(8);
-    int warps = n <= (wide ? sms : 2 * sms) ? 16 : 8;
+    // Packed sequences are uneven, and the longest is the last to end: 16 there.
+    int warps = n <= (g.ax.cu ? 4 * sms : wide ? sms : 2 * sms) ? 16 : 8;
     const long long most = ((g.ax.cu ? g.ax.ntok : g.ax.T) + kTileL - 1) / kTileL;
     while (warps > 1 && warps / 2 >= most) warps /= 2;
     return wide ? forward_cb<16, OUT, T>(g, n, warps, st) : forward_cb<8, OUT, T>(g, n, warps, st);
 }
 
-constexpr int kBwdCB = 16;
-
-template <bool GATE, typename T>
-cudaError_t backward_t(SsmArgs g, int sms, cudaStream_t st) {
+template <int CB, bool GATE, typename T>
+cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
     static PerDevice<bool> attr;
-    using M = BwdSmem<kBwdCB, T>;
-    const int tiles = ssm_backward_tiles(g.D, g.G);
+    using M = BwdSmem<CB, T>;
+    const int tiles = ssm_backward_tiles(g.D, g.G, g.ax.nseq, sms);
     const long long units = (long long)g.ax.nseq * tiles;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto kern = ssm_backward_kernel<kBwdCB, GATE, T>;
+    auto kern = ssm_backward_kernel<CB, GATE, T>;
     cudaError_t e = ensure_smem_attr(attr, kern, kSmemLimit);
     if (e != cudaSuccess) return e;
     // two CTAs of four warps fill an SM's registers (255 of a thread: the tile's six
@@ -796,7 +795,7 @@ cudaError_t backward_t(SsmArgs g, int sms, cudaStream_t st) {
     int warps = units > 2LL * sms ? 4 : 8;
     while (warps > 1 && M::bytes(g.N, warps) > (size_t)kSmemLimit) --warps;
     g.mode_x = copy_mode({{g.x, g.ld_x}, {g.dt, g.ld_dt}, {g.z, g.ld_z}, {g.dout, g.D}}, g.D / g.G, sizeof(T),
-                         kBwdCB * sizeof(T));
+                         CB * sizeof(T));
     g.mode_b = copy_mode({{g.Bm, g.ld_b}, {g.Cm, g.ld_c}}, g.N, sizeof(T), 16);
     g.mode_s = copy_mode({{g.states, g.D}}, g.D / g.G, sizeof(float), 16);
     kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
@@ -809,6 +808,17 @@ cudaError_t backward_t(SsmArgs g, int sms, cudaStream_t st) {
     return cudaSuccess;
 }
 
+// Channels of a backward CTA: 16, or 8 where that leaves SMs without one.
+int backward_channels(int D, int G, int nseq, int sms) {
+    return (long long)nseq * G * ((D / G + 15) / 16) >= sms ? 16 : 8;
+}
+
+template <bool GATE, typename T>
+cudaError_t backward_t(const SsmArgs &g, int sms, cudaStream_t st) {
+    return backward_channels(g.D, g.G, g.ax.nseq, sms) == 16 ? backward_cb<16, GATE, T>(g, sms, st)
+                                                             : backward_cb<8, GATE, T>(g, sms, st);
+}
+
 }  // namespace
 
 cudaError_t launch_ssm_forward(const SsmArgs &g, bool bf16, int sms, cudaStream_t st) {
@@ -818,7 +828,10 @@ cudaError_t launch_ssm_forward(const SsmArgs &g, bool bf16, int sms, cudaStream_
 }
 
 // Channel tiles of the backward pass over all groups.
-int ssm_backward_tiles(int D, int G) { return G * ((D / G + kBwdCB - 1) / kBwdCB); }
+int ssm_backward_tiles(int D, int G, int nseq, int sms) {
+    const int cb = backward_channels(D, G, nseq, sms);
+    return G * ((D / G + cb - 1) / cb);
+}
 
 cudaError_t launch_ssm_backward(const SsmArgs &g, bool bf16, int sms, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
