@@ -163,8 +163,8 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr unsigned kSpinLimit = 1u << 24;     // polls of a word before a warp gives up (about a second)
 
 // OUT: writes out (else only states: the walk before a backward pass without
-// recorded states). blockDim is (32, warps).
-template <int CB, bool OUT, typename T>
+// recorded states). WIDE: all rows are copied in the widest pieces. blockDim is (32, warps).
+template <int CB, bool OUT, bool WIDE, typename T>
 __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
     using M = FwdSmem<CB, T>;
     constexpr int L = M::L, NB = M::NB, NS = M::NS, LS = L / NS;   // LS: tokens of a lane outside the state loop
@@ -197,14 +197,14 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
         const int have = min(L, len - tile * L), states = min(NB, g.N - n0);
         T *r = rows_at(rh), *b = raw_at(half);
         if (n0 == 0) {
-            copy_rows<L, CB, 32>(r, x + (long long)tile * L * g.ld_x, g.ld_x, have, u.live, g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + L * CB, dt + (long long)tile * L * g.ld_dt, g.ld_dt, have, u.live, g.mode_x, lane);
+            copy_rows<L, CB, 32>(r, x + (long long)tile * L * g.ld_x, g.ld_x, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            copy_rows<L, CB, 32>(r + L * CB, dt + (long long)tile * L * g.ld_dt, g.ld_dt, have, u.live, WIDE ? kWide : g.mode_x, lane);
             if (OUT && z)
-                copy_rows<L, CB, 32>(r + 2 * L * CB, z + (long long)tile * L * g.ld_z, g.ld_z, have, u.live, g.mode_x, lane);
+                copy_rows<L, CB, 32>(r + 2 * L * CB, z + (long long)tile * L * g.ld_z, g.ld_z, have, u.live, WIDE ? kWide : g.mode_x, lane);
         }
-        copy_rows<L, NB, 32>(b, Bm + (long long)tile * L * g.ld_b + n0, g.ld_b, have, states, g.mode_b, lane);
+        copy_rows<L, NB, 32>(b, Bm + (long long)tile * L * g.ld_b + n0, g.ld_b, have, states, WIDE ? kWide : g.mode_b, lane);
         if (OUT)
-            copy_rows<L, NB, 32>(b + L * NB, Cm + (long long)tile * L * g.ld_c + n0, g.ld_c, have, states, g.mode_b, lane);
+            copy_rows<L, NB, 32>(b + L * NB, Cm + (long long)tile * L * g.ld_c + n0, g.ld_c, have, states, WIDE ? kWide : g.mode_b, lane);
     };
     if (warp < tiles) fetch(warp, 0, 0, 0);
     cp_async_commit();
@@ -403,7 +403,7 @@ struct BwdSmem {
 };
 
 // GATE: z was given. blockDim is (32, warps); a warp's p-th tile from the end.
-template <int CB, bool GATE, typename T>
+template <int CB, bool GATE, bool WIDE, typename T>
 __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
     using M = BwdSmem<CB, T>;
     constexpr int L = M::L, NB = M::NB, NS = M::NS, LS = L / NS;
@@ -442,14 +442,14 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
         const long long t = (long long)tile * L;
         T *r = rows_at(rh), *b = raw_at(half);
         if (n0 == 0) {
-            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + 2 * L * CB, dout + t * g.D, g.D, have, u.live, g.mode_x, lane);
-            if (GATE) copy_rows<L, CB, 32>(r + 3 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, g.mode_x, lane);
+            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            copy_rows<L, CB, 32>(r + 2 * L * CB, dout + t * g.D, g.D, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            if (GATE) copy_rows<L, CB, 32>(r + 3 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, WIDE ? kWide : g.mode_x, lane);
         }
-        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, g.mode_b, lane);
-        copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, g.mode_b, lane);
-        copy_rows<NB, CB, 32>(start_at(half), states0 + ((long long)tile * g.N + n0) * g.D, g.D, states, u.live, g.mode_s,
+        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, WIDE ? kWide : g.mode_b, lane);
+        copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, WIDE ? kWide : g.mode_b, lane);
+        copy_rows<NB, CB, 32>(start_at(half), states0 + ((long long)tile * g.N + n0) * g.D, g.D, states, u.live, WIDE ? kWide : g.mode_s,
                               lane);
     };
 
@@ -747,14 +747,15 @@ int copy_mode(std::initializer_list<Rows> ts, long long width, size_t es, size_t
 
 template <int CB, bool OUT, typename T>
 cudaError_t forward_cb(SsmArgs g, long long units, int warps, cudaStream_t st) {
-    static PerDevice<bool> attr;
+    static PerDevice<bool> attr[2];
     using M = FwdSmem<CB, T>;
-    auto kern = ssm_forward_kernel<CB, OUT, T>;
-    cudaError_t e = ensure_smem_attr(attr, kern, kSmemLimit);
-    if (e != cudaSuccess) return e;
     while (warps > 1 && M::bytes(g.N, warps) > (size_t)kSmemLimit) --warps;
     g.mode_x = copy_mode({{g.x, g.ld_x}, {g.dt, g.ld_dt}, {g.z, g.ld_z}}, g.D / g.G, sizeof(T), CB * sizeof(T));
     g.mode_b = copy_mode({{g.Bm, g.ld_b}, {g.Cm, g.ld_c}}, g.N, sizeof(T), 16);
+    const bool wide = g.mode_x == kWide && g.mode_b == kWide;
+    auto kern = wide ? ssm_forward_kernel<CB, OUT, true, T> : ssm_forward_kernel<CB, OUT, false, T>;
+    const cudaError_t e = ensure_smem_attr(attr[wide], kern, kSmemLimit);
+    if (e != cudaSuccess) return e;
     kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
     return cudaGetLastError();
 }
@@ -781,14 +782,11 @@ cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
 
 template <int CB, bool GATE, typename T>
 cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
-    static PerDevice<bool> attr;
+    static PerDevice<bool> attr[2];
     using M = BwdSmem<CB, T>;
     const int tiles = ssm_backward_tiles(g.D, g.G, g.ax.nseq, sms);
     const long long units = (long long)g.ax.nseq * tiles;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
-    auto kern = ssm_backward_kernel<CB, GATE, T>;
-    cudaError_t e = ensure_smem_attr(attr, kern, kSmemLimit);
-    if (e != cudaSuccess) return e;
     // two CTAs of four warps fill an SM's registers (255 of a thread: the tile's six
     // arrays and a state's decays and walk stand in them; 168 cost spills and 855 us for
     // 4 x 2048 tokens of 2048 channels against 578); eight warps where CTAs are few
@@ -798,6 +796,10 @@ cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
                          CB * sizeof(T));
     g.mode_b = copy_mode({{g.Bm, g.ld_b}, {g.Cm, g.ld_c}}, g.N, sizeof(T), 16);
     g.mode_s = copy_mode({{g.states, g.D}}, g.D / g.G, sizeof(float), 16);
+    const bool wide = g.mode_x == kWide && g.mode_b == kWide && g.mode_s == kWide;
+    auto kern = wide ? ssm_backward_kernel<CB, GATE, true, T> : ssm_backward_kernel<CB, GATE, false, T>;
+    cudaError_t e = ensure_smem_attr(attr[wide], kern, kSmemLimit);
+    if (e != cudaSuccess) return e;
     kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (g.ax.ntok) {
