@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
             const ulonglong2 *b4 = reinterpret_cast<const ulonglong2 *>(sB + ls * M::kRow);
             const ulonglong2 *c4 = reinterpret_cast<const ulonglong2 *>(sC + ls * M::kRow);
             constexpr int kB = NS * M::kRow / 4;      // vectors from one of the two states to the other
-#pragma unroll 1
+#pragma unroll 4
             for (int n = ls; n < states + ls; n += 2 * NS) {
                 unsigned long long in0 = win[0], in1 = win[NS * CB];
                 const f32x2 A0 = dup2(pa[0]), A1 = dup2(pa[NS * CB]);
