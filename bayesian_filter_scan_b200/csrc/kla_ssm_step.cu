@@ -3,6 +3,9 @@
 // (8 N bytes) for a handful of operations: HBM binds for many rows, launch
 // latency for few. `lanes` lanes (a power of two) share a channel of a row; a
 // thread walks rows with the next one's reads on their way while it works on this one.
+// Measured: 256 rows of 4096 channels, 16 states, 43 us (3.3 TB/s); one row 2.4 us.
+// Rows and channels are the grid's axes: with one axis over both, the 64-bit division
+// that takes an item apart and A's reads for every row made it 57 us.
 #include "kla_block.cuh"
 
 namespace kla {

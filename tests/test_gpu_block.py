@@ -142,6 +142,32 @@ def test_scan_many_units(B, D, T):
     check(run_scan(p, o, kw, dout, dfin, saved=True), want, scan_names(want))
 
 
+@pytest.mark.parametrize("B,D,T,N,dtype", [(160, 16, 35, 40, "bf16"), (160, 12, 18, 33, "fp32"), (120, 24, 50, 17, "bf16"),
+                                           (40, 64, 33, 128, "fp32")])
+def test_scan_many_units_of_many_states(B, D, T, N, dtype):
+    # several blocks of states, even and odd in number, on wide channel tiles
+    sp, kw, p, o, dout, dfin = scan_case([T] * B, False, D, 1, N, dtype, seed=N, strided=D == 12)
+    want = want_scan(sp, p, o, dout, dfin)
+    check(run_scan(p, o, kw, dout, dfin, saved=True), want, scan_names(want))
+
+
+def test_scan_long_row_follows_its_parts():
+    """A row of many tiles per warp equals its parts run one after the other, each from the state before it."""
+    T, D, N = 9000, 40, 16
+    sp, kw, p, o, dout, dfin = scan_case([T], False, D, 1, N, "fp32", seed=21)
+    P, O = {k: dev(v) for k, v in p.items()}, {k: dev(v) for k, v in o.items()}
+    whole, fin = kla.ssm_forward(**P, **O, final_state=True, **kw)
+    state, outs = O.pop("state0"), []
+    z = O.pop("z")
+    for a in range(0, T, 1237):
+        e = min(T, a + 1237)
+        part = {k: v[a:e] if k != "A" else v for k, v in P.items()}
+        out, state = kla.ssm_forward(**part, **O, z=z[a:e], state0=state, final_state=True, B=1, T=e - a)
+        outs.append(out)
+    # tiles start elsewhere, but every token takes the same steps
+    assert torch.equal(torch.cat(outs), whole) and torch.equal(state, fin)
+
+
 @pytest.mark.parametrize("drop", ["D", "z", "dt_bias", "state0", "all"])
 def test_scan_without_optional_inputs(drop):
     sp, kw, p, o, dout, dfin = scan_case([70, 70], False, 12, 1, 6, "fp32", seed=1)
