@@ -159,12 +159,12 @@ def test_scan_long_row_follows_its_parts():
     whole, fin = kla.ssm_forward(**P, **O, final_state=True, **kw)
     state, outs = O.pop("state0"), []
     z = O.pop("z")
-    for a in range(0, T, 1237):
-        e = min(T, a + 1237)
+    for a in range(0, T, 1232):
+        e = min(T, a + 1232)
         part = {k: v[a:e] if k != "A" else v for k, v in P.items()}
         out, state = kla.ssm_forward(**part, **O, z=z[a:e], state0=state, final_state=True, B=1, T=e - a)
         outs.append(out)
-    # tiles start elsewhere, but every token takes the same steps
+    # parts of whole tiles: every token takes the same steps
     assert torch.equal(torch.cat(outs), whole) and torch.equal(state, fin)
 
 
@@ -234,6 +234,26 @@ def test_scan_prompt_then_steps_follow_the_whole():
         q = part(t, t + 1)
         outs.append(kla.ssm_step(q["x"], q["dt"], A, q["Bm"], q["Cm"], state, D=Dk, z=q["z"], dt_bias=bias)[:, None])
     check({"out": torch.cat(outs, 1).reshape(B * T, D), "final": state}, want, {"out": "out", "final": "final"})
+
+
+def test_many_steps_of_a_slow_state_do_not_drift():
+    """A state of constant decay and input after 4000 steps, token by token and as one prompt: its decay's
+    rounding (half a unit in the last place, at random) may add up to 4000 halves at worst, its bias not."""
+    n, D, N = 4000, 8, 4
+    step = torch.full((1, D), 2.0 ** -10)
+    A = -torch.linspace(0.25, 2.0, D * N).view(D, N)
+    one, x = torch.ones(1, 1, N), torch.ones(1, D)
+    dec = torch.exp(step.double().t() * A.double())
+    h = 1.0 + (2.0 ** -10 / (1 - dec) - 1.0) * (1 - dec ** n)       # from 1 to the fixed point
+    state = torch.ones(1, D, N, device="cuda")
+    args = [t.cuda() for t in (x, step, A, one, one)]
+    for _ in range(n):
+        kla.ssm_step(*args, state, softplus=False)
+    long = [t.cuda().expand(n, *t.shape[1:]).contiguous() if i != 2 else t.cuda() for i, t in enumerate((x, step, A, one, one))]
+    _, fin = kla.ssm_forward(*long, state0=torch.ones(1, D, N, device="cuda"), softplus=False, final_state=True, B=1, T=n)
+    for got in (state, fin):
+        err = ((got.cpu().double()[0] - h) / h).abs().max()
+        assert err <= 4000 * 2.0 ** -25, float(err)
 
 
 def test_gradients_follow_differences():
