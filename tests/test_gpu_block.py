@@ -209,9 +209,11 @@ def test_scan_states_walked_again_give_the_same_gradients():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("D,G,N,strided", [(16, 1, 16, False), (18, 2, 5, True), (8, 1, 1, False), (40, 1, 128, True)])
-def test_scan_step(D, G, N, strided, dtype):
-    sp, kw, p, o, _, _ = scan_case([1] * 7, False, D, G, N, dtype, seed=N, strided=strided)
+@pytest.mark.parametrize("rows", [1, 3, 4, 7, 130])
+@pytest.mark.parametrize("D,G,N,strided", [(16, 1, 16, False), (18, 2, 5, True), (8, 1, 1, False), (40, 1, 128, True),
+                                           (22, 2, 32, True), (9, 3, 20, False), (5, 1, 8, False)])
+def test_scan_step(D, G, N, strided, rows, dtype):
+    sp, kw, p, o, _, _ = scan_case([1] * rows, False, D, G, N, dtype, seed=N, strided=strided)
     P, O = {k: dev(v) for k, v in p.items()}, {k: dev(v) for k, v in o.items()}
     state = O.pop("state0")
     out = kla.ssm_step(P["x"], P["dt"], P["A"], P["Bm"], P["Cm"], state, **O)
