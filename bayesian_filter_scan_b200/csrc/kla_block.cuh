@@ -209,6 +209,27 @@ struct Raw {
             w[0] = *reinterpret_cast<const unsigned short *>(p);
         }
     }
+    // rounded to T, two values per instruction
+    __device__ __forceinline__ void round(const float (&x)[V]) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(x[i]);
+        } else if constexpr (K == 0) {
+            w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (K == 4) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (K == 2) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (K == 1) *reinterpret_cast<uint32_t *>(p) = w[0];
+        else *reinterpret_cast<unsigned short *>(p) = (unsigned short)w[0];
+    }
     // the widened values back, exactly (they came from this type)
     __device__ __forceinline__ void set(const float (&x)[V]) {
         if constexpr (sizeof(T) == 4) {

@@ -109,7 +109,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormAr
                 float r[V];
                 rr[j].get(r);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = to_f(from_f<T>(f[i] + r[i]));
+                for (int i = 0; i < V; ++i) f[i] += r[i];
+                rr[j].round(f);
+                if (g.sum && live && (k0 + j * per_row) * V < D) rr[j].store(sum + j * per_row * V);
+                rr[j].get(f);
             }
             v[j].set(f);
             if (!live || (k0 + j * per_row) * V >= D)
@@ -149,10 +152,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormAr
             for (int j = 0; j < NV; ++j) {
                 if ((k0 + j * per_row) * V >= D) continue;
                 float f[V];
-                if (g.sum) {
-                    v[j].get(f);
-                    store_v<V>(sum + j * per_row * V, f);
-                }
                 P y;
 #pragma unroll
                 for (int k = 0; k < P::K; ++k) y.p[k] = fma2(mul2(add2(v[j].p[k], neg), r2), w[j].p[k], b[j].p[k]);
