@@ -256,7 +256,7 @@ kla_status kla_conv_backward(const kla_conv_desc *d, const void *x, const float 
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     g.x = x; g.w = weight; g.bias = bias; g.state0 = state0; g.dout = dout; g.dfinal = dfinal_state;
     g.dx = dx; g.dstate0 = dstate0; g.part = (float *)ws;
-    return of_cuda(launch_conv_backward(g, d->dtype == KLA_BF16, dweight, dbias, st));
+    return of_cuda(launch_conv_backward(g, d->dtype == KLA_BF16, sm_count(), dweight, dbias, st));
 }
 
 kla_status kla_conv_step(const kla_conv_desc *d, const void *x, const float *weight, const float *bias, void *state,

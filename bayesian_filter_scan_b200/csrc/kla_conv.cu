@@ -9,9 +9,9 @@
 // registers, so every row is read once, but for the W-1 rows in front of each run; the
 // next rows are on their way meanwhile, and a batch inside one sequence takes a path
 // without its checks. Measured: 32768 packed tokens of 2048 channels in bf16 61 us (4.4
-// TB/s); gradients of 16384 tokens 85 us (2.4 TB/s: four sums per tap and the halo of
+// TB/s); gradients of 16384 tokens 74 us (2.7 TB/s: the sums per tap and the halo on
 // both sides keep the issue slots busy); rows of odd length, one element per access,
-// take 1.3 times as long.
+// take 1.4 times as long.
 #include "kla_block.cuh"
 
 namespace kla {
@@ -19,7 +19,7 @@ namespace kla {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kBwdRun = 32;       // tokens of one thread's run, backward
+constexpr int kBwdRunMin = 16;    // tokens of one thread's shortest run, backward
 constexpr int kBwdRuns = 8;       // runs per CTA
 constexpr int kBwdBatch = 4;      // rows in flight per thread, backward
 constexpr int kBwdLanes = 32;     // channel vectors per CTA
@@ -171,12 +171,12 @@ __device__ __forceinline__ void d_pre(const ConvArgs &g, const Taps<W, V> &k, co
     }
 }
 
-// A CTA covers 32 channel vectors x 8 runs of 32 tokens. A run slides over its
+// A CTA covers 32 channel vectors x 8 runs of tokens. A run slides over its
 // tokens and the W-1 behind them (of the same sequence): dx of a token is
 // complete W-1 tokens later. The runs' sums of dweight and dbias meet in shared
 // memory in run order; the CTAs' sums are added by launch_colsum.
 template <int W, int V, typename T>
-__global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(const ConvArgs g) {
+__global__ void __launch_bounds__(kBwdLanes * kBwdRuns, V == 1 ? 3 : 2) conv_backward_kernel(const ConvArgs g, int length) {
     __shared__ float red[kBwdRuns][(W + 1) * V][kBwdLanes];
     const int lane = threadIdx.x % kBwdLanes, run = threadIdx.x / kBwdLanes;
     const int c = (blockIdx.y * kBwdLanes + lane) * V;
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns) conv_backward_kernel(con
 #pragma unroll
         for (int w = 0; w < W; ++w) dw[w][i] = 0.f;
     }
-    const long long a = ((long long)blockIdx.x * kBwdRuns + run) * kBwdRun;
-    const long long b = min(a + kBwdRun, g.ax.ntok);
+    const long long a = ((long long)blockIdx.x * kBwdRuns + run) * length;
+    const long long b = min(a + length, g.ax.ntok);
     if (live && a < b) {
         Taps<W, V> k;
         k.load(g, c);
@@ -421,12 +421,21 @@ cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
 }
 
 template <int W, int V, typename T>
-cudaError_t backward_t(const ConvArgs &g, cudaStream_t st) {
-    const int nvec = (g.D + V - 1) / V;
-    const int blocks = conv_backward_blocks(g.ax.ntok);
+cudaError_t backward_t(const ConvArgs &g, int sms, int &blocks, cudaStream_t st) {
+    const int nvec = (g.D + V - 1) / V, cols = (nvec + kBwdLanes - 1) / kBwdLanes;
+    // the run whose waves of CTAs (three per SM of the one-element kernel, two
+    // of the others, by their registers) end first; a run begins with some 24 tokens' worth of reads
+    long long best = -1;
+    int length = kBwdRunMin;
+    for (int len : {16, 24, 32, 48, 64}) {
+        const long long ctas = (g.ax.ntok + kBwdRuns * len - 1) / (kBwdRuns * len) * cols, slots = (V == 1 ? 3LL : 2LL) * sms;
+        const long long cost = (ctas + slots - 1) / slots * (len + 24);
+        if (best < 0 || cost < best) best = cost, length = len;
+    }
+    blocks = (int)((g.ax.ntok + kBwdRuns * length - 1) / (kBwdRuns * length));
     if (blocks) {
-        const dim3 grid((unsigned)blocks, (unsigned)((nvec + kBwdLanes - 1) / kBwdLanes));
-        conv_backward_kernel<W, V, T><<<grid, kBwdLanes * kBwdRuns, 0, st>>>(g);
+        const dim3 grid((unsigned)blocks, (unsigned)cols);
+        conv_backward_kernel<W, V, T><<<grid, kBwdLanes * kBwdRuns, 0, st>>>(g, length);
     }
     if (W > 1 && g.dstate0 && g.ax.nseq) {
         const dim3 grid((unsigned)g.ax.nseq, (unsigned)((g.D + kConvThreads - 1) / kConvThreads));
@@ -450,7 +459,7 @@ cudaError_t step_t(const ConvArgs &g, cudaStream_t st) {
 enum class Call { kForward, kBackward, kStep };
 
 template <int W, typename T>
-cudaError_t conv_w(const ConvArgs &g, Call call, cudaStream_t st) {
+cudaError_t conv_w(const ConvArgs &g, Call call, int sms, int &blocks, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
     const bool vec = rows_aligned(g, sizeof(T), 8);
     // 8-byte accesses, four rows ahead: 80 registers (32768 tokens of 2048 channels 70 us;
@@ -458,42 +467,45 @@ cudaError_t conv_w(const ConvArgs &g, Call call, cudaStream_t st) {
     if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, st) : forward_t<W, 1, 8, T>(g, st);
     if (call == Call::kStep) return vec ? step_t<W, V / 2, T>(g, st) : step_t<W, 1, T>(g, st);
     // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers
-    return vec ? backward_t<W, V / 2, T>(g, st) : backward_t<W, 1, T>(g, st);
+    return vec ? backward_t<W, V / 2, T>(g, sms, blocks, st) : backward_t<W, 1, T>(g, sms, blocks, st);
 }
 
 template <typename T>
-cudaError_t conv_t(const ConvArgs &g, Call call, cudaStream_t st) {
+cudaError_t conv_t(const ConvArgs &g, Call call, int sms, int &blocks, cudaStream_t st) {
     switch (g.W) {
-        case 1: return conv_w<1, T>(g, call, st);
-        case 2: return conv_w<2, T>(g, call, st);
-        case 3: return conv_w<3, T>(g, call, st);
-        default: return conv_w<4, T>(g, call, st);
+        case 1: return conv_w<1, T>(g, call, sms, blocks, st);
+        case 2: return conv_w<2, T>(g, call, sms, blocks, st);
+        case 3: return conv_w<3, T>(g, call, sms, blocks, st);
+        default: return conv_w<4, T>(g, call, sms, blocks, st);
     }
 }
 
-cudaError_t conv_any(const ConvArgs &g, bool bf16, Call call, cudaStream_t st) {
-    return bf16 ? conv_t<__nv_bfloat16>(g, call, st) : conv_t<float>(g, call, st);
+cudaError_t conv_any(const ConvArgs &g, bool bf16, Call call, int sms, int &blocks, cudaStream_t st) {
+    return bf16 ? conv_t<__nv_bfloat16>(g, call, sms, blocks, st) : conv_t<float>(g, call, sms, blocks, st);
 }
 
 }  // namespace
 
 cudaError_t launch_conv_forward(const ConvArgs &g, bool bf16, cudaStream_t st) {
-    return conv_any(g, bf16, Call::kForward, st);
+    int none = 0;
+    return conv_any(g, bf16, Call::kForward, 0, none, st);
 }
 
 int conv_backward_blocks(long long ntok) {
-    return (int)((ntok + kBwdRuns * kBwdRun - 1) / (kBwdRuns * kBwdRun));
+    return (int)((ntok + kBwdRuns * kBwdRunMin - 1) / (kBwdRuns * kBwdRunMin));
 }
 
-cudaError_t launch_conv_backward(const ConvArgs &g, bool bf16, float *dweight, float *dbias, cudaStream_t st) {
-    cudaError_t e = conv_any(g, bf16, Call::kBackward, st);
+cudaError_t launch_conv_backward(const ConvArgs &g, bool bf16, int sms, float *dweight, float *dbias, cudaStream_t st) {
+    int blocks = 0;
+    cudaError_t e = conv_any(g, bf16, Call::kBackward, sms, blocks, st);
     if (e != cudaSuccess) return e;
-    return launch_colsum(g.part, conv_backward_blocks(g.ax.ntok), (long long)g.D * (g.W + 1), (long long)g.D * g.W,
-                         dweight, g.D, dbias, nullptr, st);
+    return launch_colsum(g.part, blocks, (long long)g.D * (g.W + 1), (long long)g.D * g.W, dweight, g.D, dbias, nullptr,
+                         st);
 }
 
 cudaError_t launch_conv_step(const ConvArgs &g, bool bf16, cudaStream_t st) {
-    return conv_any(g, bf16, Call::kStep, st);
+    int none = 0;
+    return conv_any(g, bf16, Call::kStep, 0, none, st);
 }
 
 }  // namespace kla

@@ -423,14 +423,15 @@ def _tokens(name, t, like, shape):
     """A token tensor: like's dtype and device, the given shape, rows at one
     stride with contiguous values. Returns the token stride, or 0 for a
     contiguous tensor."""
+    if (t.dtype is like.dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == like.get_device()):
+        return 0
     if t.dtype is not like.dtype:
         raise TypeError("%s must have the dtype of x" % name)
     if t.get_device() != like.get_device():
         raise ValueError("%s must be on the device of x" % name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.is_contiguous():
-        return 0
     st, width = t.stride(), 1
     for n, k in zip(reversed(shape[1:]), reversed(st[1:])):
         if n > 1 and k != width:
@@ -444,14 +445,14 @@ def _tokens(name, t, like, shape):
 
 
 def _dense(name, t, like, shape, dtype=_F32):
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                     and t.get_device() == like.get_device()):
         return
     if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
     if t.get_device() != like.get_device():
         raise ValueError("%s must be on the device of x" % name)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with shape %s" % (name, tuple(shape)))
+    raise ValueError("%s must be contiguous with shape %s" % (name, tuple(shape)))
 
 
 def _axis(x, cu_seqlens, B, T):
@@ -477,7 +478,7 @@ def _axis(x, cu_seqlens, B, T):
 
 def _out_like(name, out, x, shape):
     if out is None:
-        return x.new_empty(shape)
+        return torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
     _dense(name, out, x, shape, x.dtype)
     return out
 
@@ -506,7 +507,8 @@ def conv_forward(x, weight, bias=None, state0=None, cu_seqlens=None, B=None, T=N
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
     out = _out_like("out", out, x, (x.shape[0], D))
     fs = x.new_empty((N, W - 1, D)) if final_state else None
-    _enqueue(lib().kla_conv_forward, x, ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(out), _p(fs))
+    _enqueue(lib().kla_conv_forward, x, ctypes.byref(d), x.data_ptr(), weight.data_ptr(), _p(bias), _p(state0),
+             out.data_ptr(), _p(fs))
     return (out, fs) if final_state else out
 
 
@@ -519,22 +521,22 @@ def conv_backward(x, weight, dout, bias=None, state0=None, dfinal_state=None, cu
     _dense("dout", dout, x, (x.shape[0], D), x.dtype)
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
     _dense("dfinal_state", dfinal_state, x, (N, W - 1, D), x.dtype)
-    io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
-    g = {"dx": torch.empty((x.shape[0], D), **io), "dweight": torch.empty((D, W), **f32),
-         "dbias": torch.empty(D, **f32)}
+    f32 = dict(dtype=_F32)
+    g = {"dx": x.new_empty((x.shape[0], D)), "dweight": x.new_empty((D, W), **f32),
+         "dbias": x.new_empty(D, **f32)}
     if state0 is not None:
-        g["dstate0"] = torch.empty((N, W - 1, D), **io)
+        g["dstate0"] = x.new_empty((N, W - 1, D))
     need = _bytes(lib().kla_conv_backward_workspace_bytes, x, ctypes.byref(d))
     workspace = _workspace(workspace, need, x)
-    _enqueue(lib().kla_conv_backward, x, ctypes.byref(d), _p(x), _p(weight), _p(bias), _p(state0), _p(dout),
-             _p(dfinal_state), _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]),
-             _p(g.get("dstate0")), _p(workspace), workspace.numel())
+    _enqueue(lib().kla_conv_backward, x, ctypes.byref(d), x.data_ptr(), weight.data_ptr(), _p(bias), _p(state0),
+             dout.data_ptr(), _p(dfinal_state), g["dx"].data_ptr(), g["dweight"].data_ptr(), g["dbias"].data_ptr(),
+             _p(g.get("dstate0")), workspace.data_ptr(), workspace.numel())
     return g
 
 
 def _workspace(ws, need, x):
     if ws is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        return x.new_empty(max(need, 16), dtype=torch.uint8)
     if ws.dtype != torch.uint8 or ws.device != x.device or not ws.is_contiguous() or ws.numel() < need:
         raise ValueError("workspace must be a contiguous uint8 tensor of at least %d bytes on the device of x" % need)
     return ws
@@ -580,12 +582,12 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state0=None, cu_
     d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
     _dense("state0", state0, x, (seqs, ch, N))
     out = _out_like("out", out, x, (x.shape[0], ch))
-    fs = torch.empty((seqs, ch, N), dtype=_F32, device=x.device) if final_state else None
+    fs = x.new_empty((seqs, ch, N), dtype=_F32) if final_state else None
     st = None
     if save_states:
-        st = torch.empty(lib().kla_ssm_states_bytes(ctypes.byref(d)) // 4, dtype=_F32, device=x.device)
-    _enqueue(lib().kla_ssm_forward, x, ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
-             _p(state0), _p(out), _p(fs), _p(st))
+        st = x.new_empty(lib().kla_ssm_states_bytes(ctypes.byref(d)) // 4, dtype=_F32)
+    _enqueue(lib().kla_ssm_forward, x, ctypes.byref(d), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+             Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), _p(state0), out.data_ptr(), _p(fs), _p(st))
     res = (out,) + ((fs,) if final_state else ()) + ((st,) if save_states else ())
     return res if len(res) > 1 else out
 
@@ -604,18 +606,20 @@ def ssm_backward(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, state0=No
     L = lib()
     if states is not None:
         _dense("states", states, x, (L.kla_ssm_states_bytes(ctypes.byref(d)) // 4,))
-    io, f32 = dict(dtype=x.dtype, device=x.device), dict(dtype=_F32, device=x.device)
-    g = {"dx": torch.empty((n, ch), **io), "ddt": torch.empty((n, ch), **io),
-         "dBm": torch.empty((n, G, N), **io), "dCm": torch.empty((n, G, N), **io),
-         "dA": torch.empty((ch, N), **f32), "dD": torch.empty(ch, **f32), "ddt_bias": torch.empty(ch, **f32),
-         "dstate0": torch.empty((seqs, ch, N), **f32)}
+    f32 = dict(dtype=_F32)
+    g = {"dx": x.new_empty((n, ch)), "ddt": x.new_empty((n, ch)),
+         "dBm": x.new_empty((n, G, N)), "dCm": x.new_empty((n, G, N)),
+         "dA": x.new_empty((ch, N), **f32), "dD": x.new_empty(ch, **f32), "ddt_bias": x.new_empty(ch, **f32),
+         "dstate0": x.new_empty((seqs, ch, N), **f32)}
     if z is not None:
-        g["dz"] = torch.empty((n, ch), **io)
-    workspace = _workspace(workspace, _bytes(L.kla_ssm_backward_workspace_bytes, x, ctypes.byref(d), states is not None), x)
-    _enqueue(L.kla_ssm_backward, x, ctypes.byref(d), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z), _p(dt_bias),
-             _p(state0), _p(states), _p(dout), _p(dfinal_state), _p(g["dx"]), _p(g["ddt"]),
-             _p(g["dA"]), _p(g["dBm"]), _p(g["dCm"]), _p(g["dD"]), _p(g.get("dz")),
-             _p(g["ddt_bias"]), _p(g["dstate0"]), _p(workspace), workspace.numel())
+        g["dz"] = x.new_empty((n, ch))
+    need = _bytes(L.kla_ssm_backward_workspace_bytes, x, ctypes.byref(d), states is not None)
+    workspace = _workspace(workspace, need, x)
+    _enqueue(L.kla_ssm_backward, x, ctypes.byref(d), x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+             Cm.data_ptr(), _p(D), _p(z), _p(dt_bias), _p(state0), _p(states), dout.data_ptr(), _p(dfinal_state),
+             g["dx"].data_ptr(), g["ddt"].data_ptr(), g["dA"].data_ptr(), g["dBm"].data_ptr(), g["dCm"].data_ptr(),
+             g["dD"].data_ptr(), _p(g.get("dz")), g["ddt_bias"].data_ptr(), g["dstate0"].data_ptr(),
+             workspace.data_ptr(), workspace.numel())
     return g
 
 
@@ -653,10 +657,10 @@ def layernorm_forward(x, weight=None, bias=None, residual=None, eps=1e-5, stats=
     total = _out_like("sum_out", sum_out, x, shape) if residual is not None else None
     mean = rstd = None
     if stats:
-        mean = torch.empty(shape[0], dtype=_F32, device=x.device)
-        rstd = torch.empty(shape[0], dtype=_F32, device=x.device)
-    _enqueue(lib().kla_layernorm_forward, x, ctypes.byref(d), _p(x), _p(residual), _p(weight), _p(bias), _p(out),
-             _p(total), _p(mean), _p(rstd))
+        mean = x.new_empty(shape[0], dtype=_F32)
+        rstd = x.new_empty(shape[0], dtype=_F32)
+    _enqueue(lib().kla_layernorm_forward, x, ctypes.byref(d), x.data_ptr(), _p(residual), _p(weight), _p(bias),
+             out.data_ptr(), _p(total), _p(mean), _p(rstd))
     res = (out,) + ((total,) if residual is not None else ()) + ((mean, rstd) if stats else ())
     return res if len(res) > 1 else out
 
@@ -671,13 +675,13 @@ def layernorm_backward(x, dout, mean, rstd, weight=None, dsum=None, workspace=No
     _dense("rstd", rstd, x, shape[:1])
     _dense("dout", dout, x, shape, x.dtype)
     _dense("dsum", dsum, x, shape, x.dtype)
-    f32 = dict(dtype=_F32, device=x.device)
-    g = {"dx": torch.empty(shape, dtype=x.dtype, device=x.device), "dweight": torch.empty(shape[1], **f32),
-         "dbias": torch.empty(shape[1], **f32)}
+    f32 = dict(dtype=_F32)
+    g = {"dx": x.new_empty(shape), "dweight": x.new_empty(shape[1], **f32),
+         "dbias": x.new_empty(shape[1], **f32)}
     workspace = _workspace(workspace, _bytes(lib().kla_layernorm_backward_workspace_bytes, x, ctypes.byref(d)), x)
-    _enqueue(lib().kla_layernorm_backward, x, ctypes.byref(d), _p(x), _p(weight), _p(mean), _p(rstd), _p(dout), _p(dsum),
-             _p(g["dx"]), _p(g["dweight"]), _p(g["dbias"]), _p(workspace),
-             workspace.numel())
+    _enqueue(lib().kla_layernorm_backward, x, ctypes.byref(d), x.data_ptr(), _p(weight), _p(mean), _p(rstd),
+             dout.data_ptr(), _p(dsum), g["dx"].data_ptr(), g["dweight"].data_ptr(), g["dbias"].data_ptr(),
+             workspace.data_ptr(), workspace.numel())
     return g
 
 

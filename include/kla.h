@@ -299,7 +299,11 @@ kla_status kla_backward(const kla_desc *desc,
  * not overlap inputs or each other (checked; KLA_ERR_INVALID_ARG), except where
  * a call updates a state in place. With no tokens at all, states pass through
  * and gradients of parameters are zero. All reductions have a fixed order:
- * identical inputs give bitwise identical outputs.
+ * identical inputs give bitwise identical outputs. Packed offsets are not checked
+ * on the device beyond being clamped to the axis. Make the first call of each kind
+ * on a device before any stream capture (kernel attributes and the status word's
+ * address are looked up then). The scan's waits are bounded: one that gives up
+ * ends its kernel and shows in kla_check as KLA_ERR_TIMEOUT.
  */
 
 typedef struct {

@@ -86,9 +86,9 @@ def conv(x, w, b, s0, sp, silu=True, dout=None, dfinal=None):
     lin, finl = _conv_rows(*labs, sp, False)
     ax, aw, ab, as_ = torch.autograd.grad([lin, finl], labs, [dabs, dfin.abs()], retain_graph=True, materialize_grads=True)
     ex, ew, eb, es = torch.autograd.grad([lin, finl], labs, [derr, torch.zeros_like(fin)], materialize_grads=True)
-    # a token's gradient adds W + 1 terms; a weight's sums run over 32 tokens, 8 runs,
-    # then the CTAs in 32 strided groups and those
-    chain = 32 + 8 + 32 + -(-x.shape[0] // (256 * 32)) + 4
+    # a token's gradient adds W + 1 terms; a weight's sums run over up to 64 tokens, 8 runs,
+    # then the CTAs (of 128 tokens at least) in 32 strided groups and those
+    chain = 64 + 8 + 32 + -(-x.shape[0] // (128 * 32)) + 4
     res.update(dx=(gx[tok], (W + 2) * U * ax[tok] + ex[tok]), dweight=(gw, chain * U * aw + ew),
                dbias=(gb, chain * U * ab + eb), dstate0=(gs, (W + 2) * U * as_ + es))
     return res

@@ -357,6 +357,20 @@ def test_tokens_of_no_sequence_are_left_as_they_were():
     assert torch.isfinite(c["dweight"]).all() and torch.isfinite(c["dbias"]).all() and torch.isfinite(c["dx"][:53]).all()
 
 
+def test_offsets_behind_the_axis_end_at_it():
+    sp, kw, p, o, dout, dfin = scan_case([7, 23], True, 12, 1, 6, "fp32", seed=3)
+    want = run_scan(p, o, kw, dout, dfin, saved=True)
+    far = dict(cu_seqlens=torch.tensor([0, 7, 400], dtype=torch.int32, device="cuda"))
+    got = run_scan(p, o, far, dout, dfin, saved=True)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    w = torch.randn(12, 4, generator=gen(4)).cuda()
+    x, d = dev(p["x"]), dev(dout)
+    a, b = (kla.conv_forward(x, w, final_state=True, **k) for k in (kw, far))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = (kla.conv_backward(x, w, d, **k) for k in (kw, far))
+    assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_identical_inputs_give_identical_bits():
     sp, kw, p, o, dout, dfin = scan_case([400, 90], True, 48, 1, 16, "bf16", seed=6)
     a, b = (run_scan(p, o, kw, dout, dfin, saved=True) for _ in range(2))
