@@ -239,7 +239,8 @@ struct Raw {
             w[0] = __float_as_uint(x[0]) >> 16;
         } else {
 #pragma unroll
-            for (int i = 0; i < K; ++i) w[i] = __float_as_uint(x[2 * i]) >> 16 | (__float_as_uint(x[2 * i + 1]) & 0xffff0000u);
+            for (int i = 0; i < K; ++i)
+                w[i] = __float_as_uint(x[2 * i]) >> 16 | (__float_as_uint(x[2 * i + 1]) & 0xffff0000u);
         }
     }
     __device__ __forceinline__ void get(float (&x)[V]) const {

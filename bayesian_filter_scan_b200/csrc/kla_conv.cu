@@ -27,7 +27,8 @@ constexpr int kBwdLanes = 32;     // channel vectors per CTA
 // Row `back` places before token t of the sequence that starts at s0: x, or the
 // history's row, or 0.
 template <int W, int V, typename T>
-__device__ __forceinline__ void row_before(const ConvArgs &g, int n, long long s0, long long p, int c, float (&v)[V]) {
+__device__ __forceinline__ void row_before(const ConvArgs &g, int n, long long s0, long long p, int c,
+                                           float (&v)[V]) {
     if (p >= s0) {
         load_v<V>(static_cast<const T *>(g.x) + p * g.ld_x + c, v);
     } else if (g.state0) {
@@ -428,7 +429,8 @@ cudaError_t backward_t(const ConvArgs &g, int sms, int &blocks, cudaStream_t st)
     long long best = -1;
     int length = kBwdRunMin;
     for (int len : {16, 24, 32, 48, 64}) {
-        const long long ctas = (g.ax.ntok + kBwdRuns * len - 1) / (kBwdRuns * len) * cols, slots = (V == 1 ? 3LL : 2LL) * sms;
+        const long long ctas = (g.ax.ntok + kBwdRuns * len - 1) / (kBwdRuns * len) * cols;
+        const long long slots = (V == 1 ? 3LL : 2LL) * sms;
         const long long cost = (ctas + slots - 1) / slots * (len + 24);
         if (best < 0 || cost < best) best = cost, length = len;
     }

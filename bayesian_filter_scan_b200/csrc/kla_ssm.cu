@@ -205,14 +205,14 @@ template <int CB, bool OUT, bool WIDE, typename T>
 __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
     using M = FwdSmem<CB, T>;
     constexpr int L = M::L, NB = M::NB, NS = M::NS, LS = L / NS;   // LS: tokens of a lane outside the state loop
-    constexpr int kEvery = kSsmCkpt / L;                            // tiles between recorded states
+    static_assert(L == kSsmCkpt, "every tile's start is recorded");
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x, warp = threadIdx.y, warps = blockDim.y, lc = lane % CB, ls = lane / CB;
     unsigned char *mine = smem + warp * M::warp(g.N);
-    auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };                 // [3][L][CB]
+    auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };  // [3][L][CB]
     auto raw_at = [&](int half) { return reinterpret_cast<T *>(mine + 2 * M::rows + half * M::raw); };      // [2][L][NB]
-    float *sB = reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw)), *sC = sB + M::kC;                // [NB][kRow]
-    auto words_of = [&](int w) {                                                                            // [N][CB]
+    float *sB = reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw)), *sC = sB + M::kC;  // [NB][kRow]
+    auto words_of = [&](int w) {  // [N][CB]
         return reinterpret_cast<volatile unsigned long long *>(smem + w * M::warp(g.N) + M::words);
     };
     float *sA = reinterpret_cast<float *>(smem + warps * M::warp(g.N));
@@ -229,19 +229,19 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
     const float bias = g.dt_bias ? g.dt_bias[c] : 0.f, skip = g.Dskip ? g.Dskip[c] : 0.f;
     const int len = (int)(s1 - s0), tiles = (int)(((long long)len + L - 1) / L);
 
+    const int mode_x = WIDE ? kWide : g.mode_x, mode_b = WIDE ? kWide : g.mode_b;
     // copies of one step: a block of B and C, with a tile's first block its rows
     auto fetch = [&](int tile, int n0, int rh, int half) {
         const int have = min(L, len - tile * L), states = min(NB, g.N - n0);
+        const long long t = (long long)tile * L;
         T *r = rows_at(rh), *b = raw_at(half);
         if (n0 == 0) {
-            copy_rows<L, CB, 32>(r, x + (long long)tile * L * g.ld_x, g.ld_x, have, u.live, WIDE ? kWide : g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + L * CB, dt + (long long)tile * L * g.ld_dt, g.ld_dt, have, u.live, WIDE ? kWide : g.mode_x, lane);
-            if (OUT && z)
-                copy_rows<L, CB, 32>(r + 2 * L * CB, z + (long long)tile * L * g.ld_z, g.ld_z, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, mode_x, lane);
+            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, mode_x, lane);
+            if (OUT && z) copy_rows<L, CB, 32>(r + 2 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, mode_x, lane);
         }
-        copy_rows<L, NB, 32>(b, Bm + (long long)tile * L * g.ld_b + n0, g.ld_b, have, states, WIDE ? kWide : g.mode_b, lane);
-        if (OUT)
-            copy_rows<L, NB, 32>(b + L * NB, Cm + (long long)tile * L * g.ld_c + n0, g.ld_c, have, states, WIDE ? kWide : g.mode_b, lane);
+        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, mode_b, lane);
+        if (OUT) copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, mode_b, lane);
     };
     if (warp < tiles) fetch(warp, 0, 0, 0);
     cp_async_commit();
@@ -268,13 +268,13 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
         const T *rx = rows_at(rh) + lc;
         f32x2 del[L / 2], dx[L / 2], y[L / 2];
         float sum = 0.f;           // of the tile's steps
-        // where the state behind this tile is recorded: the last, or one for the backward pass
+        // where the state behind this tile is recorded: the last one, or the next tile's start
         float *rec = nullptr;
         int rec_ld = 1;
         if (tile == tiles - 1) {
             if (g.final_state) rec = g.final_state + ((long long)u.n * g.D + c) * g.N;
-        } else if (g.states && tile % kEvery == kEvery - 1) {
-            rec = g.states + (ssm_ckpt_base(s0, u.n) + tile / kEvery + 1) * g.N * g.D + c;
+        } else if (g.states) {
+            rec = g.states + (ssm_ckpt_base(s0, u.n) + tile + 1) * g.N * g.D + c;
             rec_ld = g.D;
         }
         if (!live) rec = nullptr;
@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
             __syncwarp();
             // two states per round: two independent walks in flight
             const int at = (n0 + ls) * CB + lc;
-            volatile unsigned long long *win = words_of(warp) + at, *wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
+            volatile unsigned long long *win = words_of(warp) + at;
+            volatile unsigned long long *wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
             const float *pa = sA + at;
             const ulonglong2 *b4 = reinterpret_cast<const ulonglong2 *>(sB + ls * M::kRow);
             const ulonglong2 *c4 = reinterpret_cast<const ulonglong2 *>(sC + ls * M::kRow);
@@ -454,17 +455,17 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x, warp = threadIdx.y, warps = blockDim.y, lc = lane % CB, ls = lane / CB;
     unsigned char *mine = smem + warp * M::warp(g.N);
-    auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };                  // [4][L][CB]
+    auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };  // [4][L][CB]
     auto raw_at = [&](int half) { return reinterpret_cast<T *>(mine + 2 * M::rows + half * M::raw); };       // [2][L][NB]
-    auto start_at = [&](int half) {                                                                          // [NB][CB]
+    auto start_at = [&](int half) {  // [NB][CB]
         return reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw) + half * M::start);
     };
     float *sB = reinterpret_cast<float *>(mine + 2 * (M::rows + M::raw + M::start)), *sC = sB + M::kC;       // [NB][kRow]
-    auto words_of = [&](int w) {                                                                             // [N][CB]
+    auto words_of = [&](int w) {  // [N][CB]
         return reinterpret_cast<volatile unsigned long long *>(smem + w * M::warp(g.N) + M::words);
     };
     auto sums_of = [&](int w) { return reinterpret_cast<float *>(smem + w * M::warp(g.N) + M::sums(g.N)); };  // [N + 2][CB]
-    float *sA = reinterpret_cast<float *>(smem + warps * M::warp(g.N));                                       // [N][CB]
+    float *sA = reinterpret_cast<float *>(smem + warps * M::warp(g.N));  // [N][CB]
     const Unit u = unit_of<CB>(g);
     long long s0, s1;
     g.ax.range(u.n, s0, s1);
@@ -481,19 +482,20 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
     const int len = (int)(s1 - s0), tiles = (int)(((long long)len + L - 1) / L);
     float *part = g.part_bc + (long long)u.tile * 2 * g.N * g.ax.ntok;
 
+    const int mode_x = WIDE ? kWide : g.mode_x, mode_b = WIDE ? kWide : g.mode_b, mode_s = WIDE ? kWide : g.mode_s;
     auto fetch = [&](int tile, int n0, int rh, int half) {
         const int have = min(L, len - tile * L), states = min(NB, g.N - n0);
         const long long t = (long long)tile * L;
         T *r = rows_at(rh), *b = raw_at(half);
         if (n0 == 0) {
-            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, WIDE ? kWide : g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, WIDE ? kWide : g.mode_x, lane);
-            copy_rows<L, CB, 32>(r + 2 * L * CB, dout + t * g.D, g.D, have, u.live, WIDE ? kWide : g.mode_x, lane);
-            if (GATE) copy_rows<L, CB, 32>(r + 3 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, WIDE ? kWide : g.mode_x, lane);
+            copy_rows<L, CB, 32>(r, x + t * g.ld_x, g.ld_x, have, u.live, mode_x, lane);
+            copy_rows<L, CB, 32>(r + L * CB, dt + t * g.ld_dt, g.ld_dt, have, u.live, mode_x, lane);
+            copy_rows<L, CB, 32>(r + 2 * L * CB, dout + t * g.D, g.D, have, u.live, mode_x, lane);
+            if (GATE) copy_rows<L, CB, 32>(r + 3 * L * CB, z + t * g.ld_z, g.ld_z, have, u.live, mode_x, lane);
         }
-        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, WIDE ? kWide : g.mode_b, lane);
-        copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, WIDE ? kWide : g.mode_b, lane);
-        copy_rows<NB, CB, 32>(start_at(half), states0 + ((long long)tile * g.N + n0) * g.D, g.D, states, u.live, WIDE ? kWide : g.mode_s,
+        copy_rows<L, NB, 32>(b, Bm + t * g.ld_b + n0, g.ld_b, have, states, mode_b, lane);
+        copy_rows<L, NB, 32>(b + L * NB, Cm + t * g.ld_c + n0, g.ld_c, have, states, mode_b, lane);
+        copy_rows<NB, CB, 32>(start_at(half), states0 + ((long long)tile * g.N + n0) * g.D, g.D, states, u.live, mode_s,
                               lane);
     };
 
@@ -559,7 +561,8 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                 }
 #pragma unroll
                 for (int i = 0; i < L; i += 2) {
-                    float v[3][2] = {{d[i % LS], d[(i + 1) % LS]}, {w[i % LS], w[(i + 1) % LS]}, {o[i % LS], o[(i + 1) % LS]}};
+                    const int j = i % LS, k1 = (i + 1) % LS;
+                    float v[3][2] = {{d[j], d[k1]}, {w[j], w[k1]}, {o[j], o[k1]}};
                     if constexpr (NS > 1) {
 #pragma unroll
                         for (int k = 0; k < 6; ++k)
@@ -574,7 +577,8 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
             }
             __syncwarp();
             const int at = (n0 + ls) * CB + lc;
-            volatile unsigned long long *win = words_of(warp) + at, *wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
+            volatile unsigned long long *win = words_of(warp) + at;
+            volatile unsigned long long *wout = words_of(warp + 1 < warps ? warp + 1 : 0) + at;
             const float *pa = sA + at, *ps = start_at(half) + ls * CB + lc;
             float *psum = sums_of(warp) + at;
             const ulonglong2 *b4 = reinterpret_cast<const ulonglong2 *>(sB + ls * M::kRow);
@@ -851,7 +855,8 @@ cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
     kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (g.ax.ntok) {
-        const dim3 grid((unsigned)((g.ax.ntok + 31) / 32), (unsigned)((2 * g.N + kBcRows - 1) / kBcRows), (unsigned)g.G);
+        const unsigned rows = (2 * g.N + kBcRows - 1) / kBcRows;
+        const dim3 grid((unsigned)((g.ax.ntok + 31) / 32), rows, (unsigned)g.G);
         ssm_bc_kernel<T><<<grid, kBcRows * 32, 0, st>>>(g, tiles / g.G);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
