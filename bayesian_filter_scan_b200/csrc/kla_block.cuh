@@ -273,7 +273,7 @@ int *status_ptr();
 struct ConvArgs {
     SeqAxis ax;
     int D, W;
-    bool silu;
+    bool silu, zero_rest;
     long long ld_x;
     const void *x;
     const float *w, *bias;
@@ -300,7 +300,7 @@ inline long long ssm_ckpt_count(long long ntok, int nseq) { return ntok / kSsmCk
 struct SsmArgs {
     SeqAxis ax;
     int D, G, N;
-    bool softplus;
+    bool softplus, zero_rest;
     long long ld_x, ld_dt, ld_z, ld_b, ld_c;
     const void *x, *dt, *Bm, *Cm, *z;
     const float *A, *Dskip, *dt_bias, *state0;

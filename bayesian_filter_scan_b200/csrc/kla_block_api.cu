@@ -125,6 +125,7 @@ kla_status conv_args(const kla_conv_desc *d, ConvArgs &g, size_t &es, bool step)
     g.D = d->D;
     g.W = d->W;
     g.silu = d->silu != 0;
+    g.zero_rest = d->zero_rest != 0;
     return KLA_OK;
 }
 
@@ -143,6 +144,7 @@ kla_status ssm_args(const kla_ssm_desc *d, SsmArgs &g, size_t &es, bool step) {
     g.G = d->G;
     g.N = d->N;
     g.softplus = d->softplus != 0;
+    g.zero_rest = d->zero_rest != 0;
     return KLA_OK;
 }
 

@@ -61,13 +61,24 @@ struct Taps {
     }
 };
 
-// Grid: (token blocks, then one block row per sequence for the final states) x
-// channel blocks; a CTA is bx channel vectors x 128 / bx runs.
+// Grid: (token blocks, then one block row per sequence for the final states, then
+// blocks that clear the rows of no sequence) x channel blocks; a CTA is bx channel
+// vectors x 128 / bx runs.
 template <int W, int V, int BATCH, typename T>
-__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, int run, long long tok_blocks) {
+__global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, int run, long long tok_blocks,
+                                                                    long long seq_end) {
     const int cv = blockIdx.y * bx + threadIdx.x % bx, c = cv * V;
     if (c >= g.D) return;
     const T *x = static_cast<const T *>(g.x);
+    if (blockIdx.x >= seq_end) {
+        const long long step = (gridDim.x - seq_end) * (kConvThreads / bx);
+        const long long from = (blockIdx.x - seq_end) * (kConvThreads / bx) + threadIdx.x / bx;
+        const long long head = min((long long)g.ax.cu[0], g.ax.ntok), tail = max(g.ax.cu[g.ax.nseq], 0);
+        const float zero[V] = {};
+        for (long long t = from; t < head; t += step) store_v<V>(static_cast<T *>(g.out) + t * g.D + c, zero);
+        for (long long t = tail + from; t < g.ax.ntok; t += step) store_v<V>(static_cast<T *>(g.out) + t * g.D + c, zero);
+        return;
+    }
     if (blockIdx.x >= tok_blocks) {
         // the last W-1 inputs of one sequence
         if constexpr (W > 1) {
@@ -275,6 +286,10 @@ __global__ void __launch_bounds__(kBwdLanes * kBwdRuns, V == 1 ? 3 : 2) conv_bac
                         n = g.ax.find(t);
                         if (n < 0) {
                             s1 = t + 1;
+                            if (g.zero_rest) {
+                                const float zero[V] = {};
+                                store_v<V>(static_cast<T *>(g.dx) + t * g.D + c, zero);
+                            }
                             continue;
                         }
                         g.ax.range(n, s0, s1);
@@ -414,10 +429,12 @@ cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
     while (run > BATCH && nvec * (g.ax.ntok / run) < 148LL * 1024) run /= 2;
     const long long tok_blocks = (g.ax.ntok + (long long)runs * run - 1) / ((long long)runs * run);
     const long long seq_blocks = (W > 1 && g.final_state) ? (g.ax.nseq + runs - 1) / runs : 0;
-    if (tok_blocks + seq_blocks == 0) return cudaSuccess;
-    if (tok_blocks + seq_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(tok_blocks + seq_blocks), (unsigned)((nvec + bx - 1) / bx));
-    conv_forward_kernel<W, V, BATCH, T><<<grid, kConvThreads, 0, st>>>(g, bx, run, tok_blocks);
+    const long long rest_blocks = g.zero_rest && g.ax.cu ? (tok_blocks < 64 ? tok_blocks : 64) : 0;
+    const long long seq_end = tok_blocks + seq_blocks, blocks = seq_end + rest_blocks;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks, (unsigned)((nvec + bx - 1) / bx));
+    conv_forward_kernel<W, V, BATCH, T><<<grid, kConvThreads, 0, st>>>(g, bx, run, tok_blocks, seq_end);
     return cudaGetLastError();
 }
 

@@ -199,15 +199,27 @@ struct FwdSmem {
 constexpr int kSmemLimit = 227 * 1024;
 constexpr unsigned kSpinLimit = 1u << 24;     // polls of a word before a warp gives up (about a second)
 
+constexpr int kRestBlocks = 64;      // CTAs that clear the rows of no sequence
+
 // OUT: writes out (else only states: the walk before a backward pass without
 // recorded states). WIDE: all rows are copied in the widest pieces. blockDim is (32, warps).
+// CTAs behind the units clear the rows of no sequence.
 template <int CB, bool OUT, bool WIDE, typename T>
-__global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g) {
+__global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsigned units) {
     using M = FwdSmem<CB, T>;
     constexpr int L = M::L, NB = M::NB, NS = M::NS, LS = L / NS;   // LS: tokens of a lane outside the state loop
     static_assert(L == kSsmCkpt, "every tile's start is recorded");
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x, warp = threadIdx.y, warps = blockDim.y, lc = lane % CB, ls = lane / CB;
+    if (OUT && blockIdx.x >= units) {
+        T *out = static_cast<T *>(g.out);
+        const long long step = (long long)(gridDim.x - units) * warps * 32;
+        const long long from = ((long long)(blockIdx.x - units) * warps + warp) * 32 + lane, D = g.D;
+        const long long head = min((long long)g.ax.cu[0], g.ax.ntok), tail = max(g.ax.cu[g.ax.nseq], 0);
+        for (long long e = from; e < head * D; e += step) out[e] = from_f<T>(0.f);
+        for (long long e = tail * D + from; e < g.ax.ntok * D; e += step) out[e] = from_f<T>(0.f);
+        return;
+    }
     unsigned char *mine = smem + warp * M::warp(g.N);
     auto rows_at = [&](int half) { return reinterpret_cast<T *>(mine + half * M::rows); };  // [3][L][CB]
     auto raw_at = [&](int half) { return reinterpret_cast<T *>(mine + 2 * M::rows + half * M::raw); };      // [2][L][NB]
@@ -748,7 +760,8 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
 // dB, dC of 32 tokens of one group: the tiles' partial sums added in tile order and
 // turned through shared memory into the tensors' layout. A warp adds one (which,
 // state) row of the tokens; HBM binds (the partial sums are read once), so the loads of
-// 16 tiles are in flight at a time.
+// 16 tiles are in flight at a time. The rows of no sequence are cleared here, of all
+// gradients of tokens.
 constexpr int kBcRows = 16;      // (which, state) rows of a CTA, one per warp
 template <typename T>
 __global__ void __launch_bounds__(kBcRows * 32) ssm_bc_kernel(const SsmArgs g, int tiles) {
@@ -772,11 +785,22 @@ __global__ void __launch_bounds__(kBcRows * 32) ssm_bc_kernel(const SsmArgs g, i
     sm[warp][lane] = s;
     __syncthreads();
     const int r = threadIdx.x % kBcRows, i = threadIdx.x / kBcRows, row = r0 + r;
-    if (row >= 2 * g.N || t0 + i >= g.ax.ntok) return;
-    // tokens of no sequence keep their rows
-    if (g.ax.cu && (t0 + i < g.ax.cu[0] || t0 + i >= g.ax.cu[g.ax.nseq])) return;
+    if (t0 + i >= g.ax.ntok) return;
+    // tokens of no sequence have no partial sums
+    const bool rest = g.ax.cu && (t0 + i < g.ax.cu[0] || t0 + i >= g.ax.cu[g.ax.nseq]);
+    if (rest && !g.zero_rest) return;
+    if (rest && r0 == 0) {
+        const int per = g.D / g.G;
+        const long long at = (t0 + i) * g.D + (long long)group * per;
+        for (int c = r; c < per; c += kBcRows) {
+            static_cast<T *>(g.dx)[at + c] = from_f<T>(0.f);
+            static_cast<T *>(g.ddt)[at + c] = from_f<T>(0.f);
+            if (g.z) static_cast<T *>(g.dz)[at + c] = from_f<T>(0.f);
+        }
+    }
+    if (row >= 2 * g.N) return;
     T *o = static_cast<T *>(row < g.N ? g.dBm : g.dCm);
-    o[((t0 + i) * g.G + group) * g.N + row % g.N] = from_f<T>(sm[r][i]);
+    o[((t0 + i) * g.G + group) * g.N + row % g.N] = from_f<T>(rest ? 0.f : sm[r][i]);
 }
 
 // The widest way rows [.][width] at stride ld of several tensors can be copied in
@@ -808,7 +832,8 @@ cudaError_t forward_cb(SsmArgs g, long long units, int warps, cudaStream_t st) {
     auto kern = wide ? ssm_forward_kernel<CB, OUT, true, T> : ssm_forward_kernel<CB, OUT, false, T>;
     const cudaError_t e = ensure_smem_attr(attr[wide], kern, kSmemLimit);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)units, dim3(32, warps), M::bytes(g.N, warps), st>>>(g);
+    const unsigned rest = OUT && g.zero_rest && g.ax.cu && g.ax.ntok ? kRestBlocks : 0;
+    kern<<<(unsigned)units + rest, dim3(32, warps), M::bytes(g.N, warps), st>>>(g, (unsigned)units);
     return cudaGetLastError();
 }
 
@@ -816,7 +841,7 @@ template <bool OUT, typename T>
 cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
     const int per = g.D / g.G;
     auto units = [&](int cb) { return (long long)g.ax.nseq * g.G * ((per + cb - 1) / cb); };
-    if (units(8) > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (units(8) > 0x7fffffffLL - kRestBlocks) return cudaErrorInvalidValue;
     // 16 channels per CTA, or 8 where that leaves a quarter of the SMs without one (fewer
     // channels split the same rows into more CTAs, but share what every tile costs less:
     // with 16 and with 8 channels, 4 rows of 2048 tokens of 2048 channels took 177 and 215

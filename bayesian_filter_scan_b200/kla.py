@@ -52,7 +52,7 @@ class KlaDesc(ctypes.Structure):
 class KlaConvDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("W", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("silu", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
-                ("num_seqs", ctypes.c_int), ("ld_x", ctypes.c_longlong)]
+                ("num_seqs", ctypes.c_int), ("ld_x", ctypes.c_longlong), ("zero_rest", ctypes.c_int)]
 
 
 class KlaSsmDesc(ctypes.Structure):
@@ -60,7 +60,7 @@ class KlaSsmDesc(ctypes.Structure):
                 ("N", ctypes.c_int), ("dtype", ctypes.c_int), ("softplus", ctypes.c_int),
                 ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int), ("ld_x", ctypes.c_longlong),
                 ("ld_dt", ctypes.c_longlong), ("ld_z", ctypes.c_longlong), ("ld_b", ctypes.c_longlong),
-                ("ld_c", ctypes.c_longlong)]
+                ("ld_c", ctypes.c_longlong), ("zero_rest", ctypes.c_int)]
 
 
 class KlaNormDesc(ctypes.Structure):
@@ -502,8 +502,10 @@ def conv_forward(x, weight, bias=None, state0=None, cu_seqlens=None, B=None, T=N
     """Short causal convolution with SiLU (include/kla.h kla_conv_forward): x
     [Ntok, D] (rows may be strided), weight [D, W], bias [D]; the history state0
     [N, W-1, D] holds the inputs before each sequence. Returns ``out`` or
-    ``(out, state)`` with ``final_state``: the history after each sequence."""
+    ``(out, state)`` with ``final_state``: the history after each sequence. Rows of
+    tokens outside the offsets are 0 in a new ``out``, and stay in a given one."""
     d, D, W, N = _conv(x, weight, bias, cu_seqlens, B, T, silu)
+    d.zero_rest = out is None
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
     out = _out_like("out", out, x, (x.shape[0], D))
     fs = x.new_empty((N, W - 1, D)) if final_state else None
@@ -516,8 +518,9 @@ def conv_backward(x, weight, dout, bias=None, state0=None, dfinal_state=None, cu
                   silu=True, workspace=None):
     """Gradients of ``conv_forward`` (include/kla.h kla_conv_backward): a dict of
     ``dx`` and ``dstate0`` (x's dtype; dstate0 only with a state0) and ``dweight``,
-    ``dbias`` (fp32)."""
+    ``dbias`` (fp32). Tokens outside the offsets have gradient 0."""
     d, D, W, N = _conv(x, weight, bias, cu_seqlens, B, T, silu)
+    d.zero_rest = 1
     _dense("dout", dout, x, (x.shape[0], D), x.dtype)
     _dense("state0", state0, x, (N, W - 1, D), x.dtype)
     _dense("dfinal_state", dfinal_state, x, (N, W - 1, D), x.dtype)
@@ -578,8 +581,10 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state0=None, cu_
     [Ntok, D], Bm, Cm [Ntok, G, N] (rows may be strided), A [D, N], D and dt_bias
     [D], state0 [Nseq, D, N]. Returns ``out``, then the final state with
     ``final_state``, then what ``ssm_backward`` takes as ``states`` with
-    ``save_states``."""
+    ``save_states``. Rows of tokens outside the offsets are 0 in a new ``out``, and
+    stay in a given one."""
     d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
+    d.zero_rest = out is None
     _dense("state0", state0, x, (seqs, ch, N))
     out = _out_like("out", out, x, (x.shape[0], ch))
     fs = x.new_empty((seqs, ch, N), dtype=_F32) if final_state else None
@@ -597,8 +602,10 @@ def ssm_backward(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, state0=No
     """Gradients of ``ssm_forward`` (include/kla.h kla_ssm_backward): a dict of
     ``dx, ddt, dBm, dCm`` and ``dz`` (with z) in x's dtype, and ``dA, dD,
     ddt_bias, dstate0`` in fp32. ``states``: what the forward call returned with
-    ``save_states`` for the same inputs (walked again without)."""
+    ``save_states`` for the same inputs (walked again without). Tokens outside the
+    offsets have gradient 0."""
     d, ch, N, G, seqs = _ssm(x, dt, A, Bm, Cm, D, z, dt_bias, cu_seqlens, B, T, softplus)
+    d.zero_rest = 1
     n = x.shape[0]
     _dense("dout", dout, x, (n, ch), x.dtype)
     _dense("state0", state0, x, (seqs, ch, N))

@@ -293,8 +293,9 @@ kla_status kla_backward(const kla_desc *desc,
  * in elements, so a tensor may be a column slice of a wider projection; 0 stands
  * for a contiguous tensor. Sequences are B rows of T tokens, or num_seqs packed
  * sequences with cu_seqlens as in kla_desc (a sequence may be empty; tokens
- * before the first offset or behind the last one belong to none: their output
- * rows are left as they were and they enter no sum). Pointers need the alignment of
+ * before the first offset or behind the last one belong to none: they enter no
+ * sum, and their rows of outputs and gradients are left as they were, or set to 0
+ * with zero_rest). Pointers need the alignment of
  * their element type only; 16-byte aligned rows move as vectors. Outputs may
  * not overlap inputs or each other (checked; KLA_ERR_INVALID_ARG), except where
  * a call updates a state in place. With no tokens at all, states pass through
@@ -314,6 +315,7 @@ typedef struct {
     const int *cu_seqlens;
     int num_seqs;
     long long ld_x;         /* token stride of x */
+    int zero_rest;          /* nonzero: rows of tokens of no sequence become 0 */
 } kla_conv_desc;
 
 /* Depthwise causal convolution with SiLU (Kalman Linear Attention, technical
@@ -354,6 +356,7 @@ typedef struct {
     const int *cu_seqlens;
     int num_seqs;
     long long ld_x, ld_dt, ld_z, ld_b, ld_c;  /* token strides of x, dt, z, Bm, Cm */
+    int zero_rest;          /* as in kla_conv_desc */
 } kla_ssm_desc;
 
 /* Selective state space scan: a diagonal linear recurrence whose step delta and

@@ -1,0 +1,61 @@
+"""The recurrent block where it can go wrong beside its values: padded packed axes,
+accuracy of the functions of one argument, captured single tokens, waits that run
+out, and the block's operators around the Kalman mixer."""
+import pytest
+import torch
+
+from bayesian_filter_scan_b200 import kla
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture
+def poisoned():
+    """New tensors are filled with NaN instead of whatever was in their memory."""
+    torch.use_deterministic_algorithms(True)
+    was = torch.utils.deterministic.fill_uninitialized_memory
+    torch.utils.deterministic.fill_uninitialized_memory = True
+    yield
+    torch.utils.deterministic.fill_uninitialized_memory = was
+    torch.use_deterministic_algorithms(False)
+
+
+# ---- padded packed axes -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,G,N,cu,n", [
+    (16, 1, 8, [0, 20, 53], 62), (9, 3, 5, [3, 3, 40], 57), (24, 1, 33, [5, 30, 30], 31), (40, 2, 16, [70, 75, 75], 200),
+    (8, 1, 4, [6, 6], 20), (264, 1, 16, [130, 131, 400], 431)])
+def test_rows_of_no_sequence_are_zero_in_new_tensors(poisoned, D, G, N, cu, n, dtype):
+    g = torch.Generator().manual_seed(n)
+    t = DT[dtype]
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, z, dt, dout = (r(n, D).to(t).cuda() for _ in range(4))
+    Bm, Cm = (r(n, G, N).to(t).cuda() for _ in range(2))
+    A, w = -torch.rand(D, N, generator=g).cuda(), r(D, 4).cuda()
+    out_of = torch.ones(n, dtype=torch.bool)
+    out_of[cu[0]:cu[-1]] = False
+    for v in (x, z, dt, dout, Bm, Cm):      # what lies there enters nothing
+        v[out_of.cuda()] = float("nan")
+    kw = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    y, st = kla.ssm_forward(x, dt, A, Bm, Cm, z=z, save_states=True, **kw)
+    u = kla.conv_forward(x, w, **kw)
+    c = kla.conv_backward(x, w, dout, **kw)
+    res = {"out": y, "u": u, "conv dx": c["dx"], "dweight": c["dweight"], "dbias": c["dbias"]}
+    for gate, states in ((z, st), (None, None)):
+        s = kla.ssm_backward(x, dt, A, Bm, Cm, dout, z=gate, states=states, **kw)
+        res.update({"%s %d" % (k, gate is not None): v for k, v in s.items()})
+    torch.cuda.synchronize()
+    for k, v in res.items():
+        assert torch.isfinite(v.float()).all(), k
+        if v.shape[0] == n:
+            assert not v.cpu()[out_of].any(), k
+    # a given output keeps them
+    mine = torch.full((n, D), 7.0, dtype=t, device="cuda")
+    kla.ssm_forward(x, dt, A, Bm, Cm, z=z, out=mine, **kw)
+    assert (mine.cpu()[out_of] == 7).all() and torch.equal(mine.cpu()[~out_of], y.cpu()[~out_of])
+    mine.fill_(7.0)
+    kla.conv_forward(x, w, out=mine, **kw)
+    assert (mine.cpu()[out_of] == 7).all() and torch.equal(mine.cpu()[~out_of], u.cpu()[~out_of])
