@@ -49,8 +49,6 @@ constexpr int kTileL = 16;       // tokens of a tile
 constexpr int kTileNB = 16;      // states whose B and C a warp stages at once
 constexpr int kLdPad = 4;        // floats behind a state's tokens in shared memory: states on other banks
 
-__device__ __forceinline__ float sigmoid_a(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
-
 // How rows reach shared memory: pieces of 16 bytes (or a whole narrower row), of 4
 // bytes, or single elements, by the alignment of the rows.
 enum : int { kScalar = 0, kWord = 1, kWide = 2 };
@@ -429,7 +427,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsig
 #pragma unroll
             for (int i = 0; i < LS; ++i) {
                 v[i] = fmaf(skip, xs[i], v[i]);
-                if (z) v[i] *= zs[i] * sigmoid_a(zs[i]);
+                if (z) v[i] *= zs[i] * sigmoid_for<T>(zs[i]);
             }
             T *out = static_cast<T *>(g.out) + (s0 + tile * L + ls * LS) * g.D + c;
             const int mine_n = live ? have - ls * LS : 0;
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                     o[i] = to_f(rx[(2 * L + t) * CB]);
                     if (GATE) {
                         const float zz = to_f(rx[(3 * L + t) * CB]);
-                        o[i] *= zz * sigmoid_a(zz);
+                        o[i] *= zz * sigmoid_for<T>(zz);
                     }
                 }
                 if (g.softplus) {
@@ -719,11 +717,11 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                 const int j = i + k;
                 float o = os[j], dz = 0.f;
                 if (GATE) {
-                    const float sg = sigmoid_a(zs[j]), full = fmaf(skip, xs[j], vy[j]);
+                    const float sg = sigmoid_for<T>(zs[j]), full = fmaf(skip, xs[j], vy[j]);
                     dz = o * full * sg * fmaf(zs[j], 1.f - sg, 1.f);
                     o *= zs[j] * sg;
                 }
-                const float dd = fmaf(vu[j], xs[j], vd[j]) * (g.softplus ? sigmoid_a(rs[j]) : 1.f);
+                const float dd = fmaf(vu[j], xs[j], vd[j]) * (g.softplus ? sigmoid_for<T>(rs[j]) : 1.f);
                 if (j < mine_n) {
                     const long long at = row + (long long)j * g.D;
                     static_cast<T *>(g.dx)[at] = from_f<T>(fmaf(vu[j], st[k], skip * o));

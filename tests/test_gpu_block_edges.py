@@ -59,3 +59,47 @@ def test_rows_of_no_sequence_are_zero_in_new_tensors(poisoned, D, G, N, cu, n, d
     mine.fill_(7.0)
     kla.conv_forward(x, w, out=mine, **kw)
     assert (mine.cpu()[out_of] == 7).all() and torch.equal(mine.cpu()[~out_of], u.cpu()[~out_of])
+
+
+# ---- functions of one argument -----------------------------------------------------
+# One token of one state from zero, with steps, inputs, B and C of 1, leaves exactly
+# the function that is looked at in an output or a gradient.
+
+RANGES = [(-1, 1), (-8, -1), (-30, -8), (-80, -30), (1, 20)]
+
+
+def one_token(D):
+    one = torch.ones(1, D, device="cuda")
+    return one, torch.ones(1, 1, 1, device="cuda"), -torch.ones(D, 1, device="cuda")
+
+
+def arguments(D, lo, hi):
+    return (lo + (hi - lo) * torch.rand(1, D, generator=torch.Generator().manual_seed(D + hi))).cuda()
+
+
+def near(got, want, bound, what):
+    err = ((got.double() - want).abs() - bound).max()
+    assert err <= 0, (what, float(err), float(((got.double() - want) / want).abs().max()))
+
+
+@pytest.mark.parametrize("lo,hi", RANGES)
+@pytest.mark.parametrize("D", [64, 4096])
+def test_fp32_gate_and_slopes(D, lo, hi):
+    """sigmoid: an exponential within 2 U (one unit in the last place), the sum 1 U, the quotient 4 U (two units).
+    With U = 2^-24: 7 U, one more for each product behind it."""
+    one, bc, A = one_token(D)
+    z = arguments(D, lo, hi)
+    zd = z.double()
+    s = torch.sigmoid(zd)
+    args = (one, one, A, bc, bc)
+    out, st = kla.ssm_forward(*args, z=z, softplus=False, save_states=True)
+    near(out, zd * s, 9 * ob.U * (zd * s).abs(), "gate of a prompt")
+    state = torch.zeros(1, D, 1, device="cuda")
+    near(kla.ssm_step(*args, state, z=z, softplus=False), zd * s, 9 * ob.U * (zd * s).abs(), "gate of a step")
+    g = kla.ssm_backward(*args, one, z=z, states=st, softplus=False)
+    # s (1 + z (1 - s)): 1 - s within 7 U s + U, the product with z and the sum, both factors
+    near(g["dz"], s * (1 + zd * (1 - s)), 18 * ob.U * s * (1 + zd.abs()), "slope of the gate")
+    near(g["dx"], zd * s, 10 * ob.U * (zd * s).abs(), "gate in the gradient of x")
+    # a step dt = z through softplus: its slope is sigmoid(z)
+    g = kla.ssm_backward(one, z, A, bc, bc, one)
+    near(g["ddt"], s, 8 * ob.U * s, "slope of softplus")
