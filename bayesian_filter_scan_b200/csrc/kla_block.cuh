@@ -152,20 +152,27 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 __device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
 
 // softplus(x) = max(x, 0) + log(1 + y) of two values, y = e^-|x| in (0, 1]. log(1 + y)
-// is y times a polynomial of degree 9 fitted to log(1 + y) / y on [0, 1] for the least
-// relative error (5e-9; 1.5e-7 with fp32's rounding), so a small y keeps its digits,
-// which the logarithm of a rounded 1 + y would not.
+// is y times a polynomial of degree 9 with p(0) = 1, fitted to log(1 + y) / y on [0, 1]
+// for the least relative error (iteratively reweighted least squares; each coefficient is
+// rounded to fp32 before the ones behind it are fitted again). These coefficients are
+// within 5.3e-9, without a side; 9.6e-8 with fp32's rounding. A small y keeps its digits
+// that way, which the logarithm of a rounded 1 + y would not. T is the tensors' type: for
+// bf16, whose steps are known to 2^-9, y comes from the approximated power of two, whose
+// rounded exponent makes it |x| 2^-24 off (relative; 1e-6 at x = -12).
+template <typename T>
 __device__ __forceinline__ void softplus2(float &x0, float &x1) {
-    const f32x2 y = pack2(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
-    f32x2 p = dup2(-0.0032439809f);
-    p = fma2(p, y, dup2(0.019851264f));
-    p = fma2(p, y, dup2(-0.05695916f));
-    p = fma2(p, y, dup2(0.10603617f));
-    p = fma2(p, y, dup2(-0.1530557f));
-    p = fma2(p, y, dup2(0.19675931f));
-    p = fma2(p, y, dup2(-0.24954133f));
-    p = fma2(p, y, dup2(0.33329964f));
-    p = fma2(p, y, dup2(-0.499999f));
+    f32x2 y;
+    if constexpr (sizeof(T) == 4) y = pack2(expf(-fabsf(x0)), expf(-fabsf(x1)));
+    else y = pack2(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
+    f32x2 p = dup2(-0.0033065395f);
+    p = fma2(p, y, dup2(0.020150334f));
+    p = fma2(p, y, dup2(-0.057561528f));
+    p = fma2(p, y, dup2(0.10670013f));
+    p = fma2(p, y, dup2(-0.15349098f));
+    p = fma2(p, y, dup2(0.19693193f));
+    p = fma2(p, y, dup2(-0.24958156f));
+    p = fma2(p, y, dup2(0.3333047f));
+    p = fma2(p, y, dup2(-0.4999993f));
     p = fma2(p, y, dup2(1.f));
     float m0, m1;
     unpack2(fma2(p, y, pack2(fmaxf(x0, 0.f), fmaxf(x1, 0.f))), m0, m1);

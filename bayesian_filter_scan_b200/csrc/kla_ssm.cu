@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsig
                 }
                 if (g.softplus) {
 #pragma unroll
-                    for (int i = 0; i < LS; i += 2) softplus2(d[i], d[i + 1]);
+                    for (int i = 0; i < LS; i += 2) softplus2<T>(d[i], d[i + 1]);
                 }
 #pragma unroll
                 for (int i = 0; i < LS; ++i) w[i] *= d[i];
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                 }
                 if (g.softplus) {
 #pragma unroll
-                    for (int i = 0; i < LS; i += 2) softplus2(d[i], d[i + 1]);
+                    for (int i = 0; i < LS; i += 2) softplus2<T>(d[i], d[i + 1]);
                 }
 #pragma unroll
                 for (int i = 0; i < LS; ++i) w[i] *= d[i];
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
 #pragma unroll
         for (int i = 0; i < LS; i += 2) {
             float st[2] = {rs[i], rs[i + 1]};
-            if (g.softplus) softplus2(st[0], st[1]);
+            if (g.softplus) softplus2<T>(st[0], st[1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int j = i + k;

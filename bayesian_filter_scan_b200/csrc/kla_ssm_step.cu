@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs g,
         float y = 0.f;
         if (live) {
             float del = to_f(cur.dt) + bias, spare = 0.f;
-            if (g.softplus) softplus2(del, spare);
+            if (g.softplus) softplus2<T>(del, spare);
             const float dx = del * to_f(cur.x);
             for (int n = l * V; n < g.N; n += lanes * V) {
                 if (lanes * V < g.N) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_rows_kernel(const SsmAr
             del = to_f(static_cast<const T *>(g.dt)[own * g.ld_dt + c]) + bias;
             if (g.z) z = to_f(static_cast<const T *>(g.z)[own * g.ld_z + c]);
         }
-        if (g.softplus) softplus2(del, spare);
+        if (g.softplus) softplus2<T>(del, spare);
         const float dx = del * x;
         float y[R];
         const int first = (threadIdx.x & 31) - l;

@@ -1,0 +1,34 @@
+"""The polynomials of the recurrent block's kernels, from the coefficients that the
+sources hold, in fp64: within the errors that the sources state."""
+import os
+import re
+
+import numpy as np
+
+from bayesian_filter_scan_b200 import build as kbuild
+
+
+def coefficients(source, function):
+    """Lowest power first: the function sets p to its highest coefficient and folds in the others."""
+    text = open(os.path.join(kbuild.CSRC, source)).read()
+    body = text[text.index(" %s(float &" % function):]
+    body = body[:body.index("\n}\n")]
+    first = re.search(r"f32x2 p = dup2\((\S+?)f\)", body).group(1)
+    rest = re.findall(r"p = fma2\(p, \w, dup2\((\S+?)f\)\)", body)
+    return [float(np.float32(c)) for c in [first] + rest][::-1]
+
+
+def relative(c, x, want):
+    return np.polynomial.polynomial.polyval(x, np.array(c)) / want - 1
+
+
+def check(c, x, want, bound):
+    assert c[0] == 1.0
+    assert np.abs(relative(c, x, want)).max() <= bound
+
+
+def test_softplus_polynomial():
+    c = coefficients("kla_block.cuh", "softplus2")
+    assert len(c) == 10
+    y = np.linspace(0, 1, 100001)[1:]
+    check(c, y, np.log1p(y) / y, 5.3e-9)

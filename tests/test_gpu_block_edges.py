@@ -103,3 +103,15 @@ def test_fp32_gate_and_slopes(D, lo, hi):
     # a step dt = z through softplus: its slope is sigmoid(z)
     g = kla.ssm_backward(one, z, A, bc, bc, one)
     near(g["ddt"], s, 8 * ob.U * s, "slope of softplus")
+
+
+@pytest.mark.parametrize("lo,hi", RANGES)
+@pytest.mark.parametrize("D", [64, 4096])
+def test_fp32_softplus(D, lo, hi):
+    """The exponential within 2 U, log(1 + y) no steeper than y, its polynomial within 5.3e-9 and 2 U of rounding,
+    the last sum 1 U."""
+    one, bc, A = one_token(D)
+    dt = arguments(D, lo, hi)
+    want = torch.logaddexp(dt.double(), torch.zeros_like(dt, dtype=torch.float64))
+    near(kla.ssm_forward(one, dt, A, bc, bc), want, 6 * ob.U * want, "prompt")
+    near(kla.ssm_step(one, dt, A, bc, bc, torch.zeros(1, D, 1, device="cuda")), want, 6 * ob.U * want, "step")
