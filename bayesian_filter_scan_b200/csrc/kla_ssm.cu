@@ -154,14 +154,20 @@ __device__ __forceinline__ void reduce_halving(float (&v)[M], int lane) {
     }
 }
 
-// The approximated power of two is 2e-8 to 5e-8 low on average, which a state that
-// remembers thousands of tokens would add up (a relative 2e-5 after a thousand). What a
-// tile hands on therefore decays by the power of two of the tile's whole exponent: the
-// product of its 16 decays, which the walk applied, is taken out and that one put in,
-// (2^(A sum delta) - prod a) h_start on top of the walk's end. One error in 16 tokens
-// instead of 16, for 12 instructions of a state's 100: the states after 9001 packed
-// tokens are within 7e-7 of the 64-bit recurrence, 3.4e-6 without, and the gradient of A
-// within 6e-7, 1.9e-6 without; 8 rows of 4096 tokens take 548 us, 520 without.
+// The approximated power of two is low on average: by 2e-8 for exponents from -1 to -0.01
+// and 5e-8 below -1 (1e-8 next to 0). A state that remembers thousands of tokens would add
+// that up (a relative 2e-5 after a thousand), and an input's share in the state passes up
+// to 16 of them in its own tile. So every exponent is raised by 2.5e-8, which costs nothing
+// (a fused multiply-add in place of a product) and leaves a mean between -5e-9 and +1e-8
+// for exponents from -1 on, those that are remembered; 2^0 stays exactly 1, which
+// steps of zero need. And what a tile hands on decays by the power of two of the tile's
+// whole exponent: the product of its 16 decays, which the walk applied, is taken out and
+// that one put in, (2^(A sum delta) - prod a) h_start on top of the walk's end: one rounding
+// in 16 tokens instead of 16, for 12 instructions of a state's 100. The states after 9001
+// packed tokens are within 5.0e-7 of the 64-bit recurrence (7.0e-7 without the raised
+// exponents, 3.4e-6 without either), the gradient of A of 1403 tokens of 64 states within
+// 2.8e-7 (5.7e-7); 8 rows of 4096 tokens take 550 us, 520 without the tile's exponent.
+constexpr float kEx2Low = 2.5e-8f;
 __device__ __forceinline__ float product_of(const f32x2 (&a)[kTileL / 2]) {
     const f32x2 p = mul2(mul2(mul2(a[0], a[1]), mul2(a[2], a[3])), mul2(mul2(a[4], a[5]), mul2(a[6], a[7])));
     float lo, hi;
@@ -350,12 +356,13 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsig
 #pragma unroll
                 for (int i = 0; i < L / 2; ++i) {
                     float e0, e1, f0, f1;
-                    unpack2(mul2(del[i], A0), e0, e1);
-                    unpack2(mul2(del[i], A1), f0, f1);
+                    unpack2(fma2(del[i], A0, dup2(kEx2Low)), e0, e1);
+                    unpack2(fma2(del[i], A1, dup2(kEx2Low)), f0, f1);
                     a0[i] = pack2(ex2(e0), ex2(e1));
                     a1[i] = pack2(ex2(f0), ex2(f1));
                 }
-                const float fix0 = ex2(sum * A2_0) - product_of(a0), fix1 = ex2(sum * A2_1) - product_of(a1);
+                const float fix0 = ex2(fmaf(sum, A2_0, kEx2Low)) - product_of(a0);
+                const float fix1 = ex2(fmaf(sum, A2_1, kEx2Low)) - product_of(a1);
                 // the states before the tile, once the warp that has the tile before has left them
                 for (unsigned spin = 0; !__all_sync(0xffffffffu, (unsigned)(in0 >> 32) == (unsigned)tile &&
                                                                      (unsigned)(in1 >> 32) == (unsigned)tile);) {
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                     for (int k = 0; k < 2; ++k) {
                         const int i = 2 * q4 + k;
                         float e0, e1, u0, u1;
-                        unpack2(mul2(del[i], A22), e0, e1);
+                        unpack2(fma2(del[i], A22, dup2(kEx2Low)), e0, e1);
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         a[i] = pack2(e0, e1);
@@ -636,7 +643,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                         return;
                     }
                 }
-                const float first = __uint_as_float((unsigned)in), fix = ex2(sum * An * kLog2e) - product_of(a);
+                const float first = __uint_as_float((unsigned)in), fix = ex2(fmaf(sum, An * kLog2e, kEx2Low)) - product_of(a);
                 float q = first;
                 f32x2 dA = 0;
                 const f32x2 An2 = dup2(An);

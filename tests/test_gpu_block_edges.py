@@ -115,3 +115,40 @@ def test_fp32_softplus(D, lo, hi):
     want = torch.logaddexp(dt.double(), torch.zeros_like(dt, dtype=torch.float64))
     near(kla.ssm_forward(one, dt, A, bc, bc), want, 6 * ob.U * want, "prompt")
     near(kla.ssm_step(one, dt, A, bc, bc, torch.zeros(1, D, 1, device="cuda")), want, 6 * ob.U * want, "step")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [16, 160])
+@pytest.mark.parametrize("D", [1024, 8192])
+def test_decays_have_no_side(D, T, dtype):
+    """States of slow decays (2^-0.1 to 2^-0.01 a token), all terms positive: the error's mean over the channels. A
+    decay may be off by 1e-8 on average, so a result by that times the decays that it holds: its sensitivity to
+    them, taken from the 64-bit recurrence with decays 1e-6 larger. 1e-8 more for the mean of the roundings (each
+    result 1e-7 at random, a thousand channels or more)."""
+    g = torch.Generator().manual_seed(T + D)
+    dt = (0.02 + 0.08 * torch.rand(T, D, generator=g)).to(DT[dtype])
+    A = -torch.exp(torch.linspace(-1.2, 0.0, D))[:, None] * 0.6931
+    one = torch.ones(T, D, dtype=DT[dtype], device="cuda")
+    bc = torch.ones(T, 1, 1, dtype=DT[dtype], device="cuda")
+    args = (one, dt.cuda(), A.cuda(), bc, bc)
+    out, fin, st = kla.ssm_forward(*args, softplus=False, final_state=True, save_states=True)
+    grad = kla.ssm_backward(*args, one, states=st, softplus=False)
+
+    def exact(grow):
+        d, a = dt.double(), A.double().requires_grad_()
+        dec = torch.exp(d * a[:, 0]) * (1 + grow)
+        h, ys = torch.zeros(D, dtype=torch.float64), []
+        for t in range(T):
+            h = dec[t] * h + d[t]
+            ys.append(h)
+        dA, = torch.autograd.grad(sum(y.sum() for y in ys), a)
+        return {"out": ys[-1].detach(), "final": h.detach(), "dA": dA[:, 0]}
+
+    want, more = exact(0.0), exact(1e-6)
+    got = {"final": fin[0, :, 0], "dA": grad["dA"][:, 0]}
+    if dtype == "fp32":
+        got["out"] = out[-1]
+    for k, v in got.items():
+        held = float(((more[k] - want[k]) / want[k] / 1e-6).mean())
+        mean = float(((v.double().cpu() - want[k]) / want[k]).mean())
+        assert held > 2 and abs(mean) <= 1e-8 * held + 1e-8, (k, mean, held)
