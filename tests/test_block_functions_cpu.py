@@ -32,3 +32,10 @@ def test_softplus_polynomial():
     assert len(c) == 10
     y = np.linspace(0, 1, 100001)[1:]
     check(c, y, np.log1p(y) / y, 5.3e-9)
+
+
+def test_power_of_two_polynomial():
+    c = coefficients("kla_ssm_step.cu", "exp2_near")
+    assert len(c) == 7
+    f = np.linspace(-0.5, 0.5, 100001)
+    check(c, f, np.exp2(f), 3.0e-9)

@@ -152,3 +152,21 @@ def test_decays_have_no_side(D, T, dtype):
         held = float(((more[k] - want[k]) / want[k] / 1e-6).mean())
         mean = float(((v.double().cpu() - want[k]) / want[k]).mean())
         assert held > 2 and abs(mean) <= 1e-8 * held + 1e-8, (k, mean, held)
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 1), (1, 10), (10, 80)])
+@pytest.mark.parametrize("N", [1, 4, 16])
+def test_one_decay(N, lo, hi):
+    """A state of 1 after one token without input. The exponent: log2(e) in fp32 is 0.25 U off, its products with A and
+    with the step round twice, so 2.25 U of |delta A|; the power of two within 4 U of a prompt, 1.2 U of a step."""
+    D = 1024
+    one, bc = torch.zeros(1, D, device="cuda"), torch.ones(1, 1, N, device="cuda")
+    d = arguments(D, lo, hi).abs()
+    A = -torch.ones(D, N, device="cuda") + 0.5 * torch.rand(D, N, generator=torch.Generator().manual_seed(N)).cuda()
+    x = d.double().t() * A.double()
+    want = torch.exp(x)[None]
+    state = torch.ones(1, D, N, device="cuda")
+    _, fin = kla.ssm_forward(one, d, A, bc, bc, state0=state, softplus=False, final_state=True)
+    near(fin, want, (4 + 2.3 * x.abs()) * ob.U * want, "prompt")
+    kla.ssm_step(one, d, A, bc, bc, state, softplus=False)
+    near(state, want, (1.2 + 2.3 * x.abs()) * ob.U * want, "step")
