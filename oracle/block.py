@@ -3,11 +3,11 @@ selective scan, layer norm): test infrastructure, on the CPU, from the formulas,
 one token after the other, with gradients by automatic differentiation.
 
 Every function returns values and, beside each, a slack: a bound on how far a
-correct fp32 evaluation may be off before its result is rounded. It is a count
-of fp32 roundings times the sum of the absolute values of the terms that enter
-the result, which the references get by running the same formulas on absolute
-values. U is one rounding (2^-24, relative); functions of one argument (exp,
-softplus, sigmoid) are within 8 U, an approximated power of two within 2^-22.
+correct fp32 evaluation may be off before its result is rounded. It counts fp32
+roundings, each times the absolute value of the term that it rounds; the scan
+carries them along its recurrence. U is one rounding (2^-24, relative);
+functions of one argument (exp, softplus, sigmoid) are within 8 U, an
+approximated power of two within 2^-22.
 """
 from __future__ import annotations
 
@@ -133,71 +133,130 @@ def scan(x, dt, A, Bm, Cm, sp, Dskip=None, z=None, dt_bias=None, h0=None, softpl
     lx, la, lb, lA, lB, lC, lD, lg, lh = leaves = [
         t.clone().requires_grad_() for t in (x, step, step, A, Bm, Cm, Dskip, gate, h0)]
     out, fin, pre = _scan_rows(lx, la, lb, lA, lB, lC, lD, lg, lh, sp)
-    absl = [t.clone().requires_grad_() for t in
-            (x.abs(), step, step.abs(), A, Bm.abs(), Cm.abs(), Dskip.abs(), gate.abs(), h0.abs())]
-    aout, afin, apre = _scan_rows(*absl, sp)
-    longest = max([e - a for a, e in sp] + [1])
-    # A decay's relative error: its power of two (2^-22), its exponent's two roundings and
-    # delta's error, at an exponent of at most E where the decay still counts, and the rounding
-    # of its product; a path of up to `longest` decays adds them up, twice over where the
-    # ranges' maps are joined. Decays below e^-40 leave nothing that counts.
-    E = float(torch.clamp(-(step[..., None] * A), 0, 40).max()) if x.shape[0] else 0.0
-    k = longest * (4 + 12 * E + 4) * 2 * U + (N + 24) * U
     rows = torch.cat([torch.arange(a, e) for a, e in sp]) if sp else torch.zeros(0, dtype=torch.long)
-    res = {"out": (out.detach(), (k + 16 * U) * aout.detach()), "final": (fin.detach(), k * afin.detach())}
+    go = None if dout is None else dout.double()
+    gf = None if dout is None else torch.zeros_like(fin) if dfinal is None else dfinal.double()
+    err = _scan_errors(x, raw, step, slope, A, Bm, Cm, Dskip, z, gate, h0, sp, softplus, go, gf)
+    res = {"out": (out.detach(), err["out"][rows]), "final": (fin.detach(), err["final"])}
     if dout is None:
         return res
-    go = dout.double()[rows]
-    gf = torch.zeros_like(fin) if dfinal is None else dfinal.double()
-    gx, ga, gb, gA, gB, gC, gD, gg, gh = torch.autograd.grad([out, fin], leaves, [go, gf], materialize_grads=True)
-    ax, aa, ab, aA, aB, aC, aD, ag, ah = torch.autograd.grad([aout, afin], absl, [go.abs(), gf.abs()], materialize_grads=True)
-    # the adjoint's paths meet the forward's: twice the chain; the decay's gradient with |A|
-    aa, flush_a, flush_A = _abs_decay_grad(absl, sp, go.abs(), gf.abs())
-    k2 = 2 * k + 48 * U
-    tok_sum = (x.shape[0] + 64) * U
-    res.update(
-        dx=(gx[rows], k2 * ax[rows]), dBm=(gB[rows], (k2 + D * U) * aB[rows]), dCm=(gC[rows], (k2 + D * U) * aC[rows]),
-        dA=(gA, (k2 + tok_sum) * aA.abs() + flush_A), dD=(gD, (k2 + tok_sum) * aD),
-        dstate0=(gh, k2 * ah))
+    gx, ga, gb, gA, gB, gC, gD, gg, gh = torch.autograd.grad([out, fin], leaves, [go[rows], gf], materialize_grads=True)
     ddt = (ga + gb) * slope
-    addt = (aa + ab) * slope
-    eddt = k2 * addt + flush_a * slope
-    res["ddt"] = (ddt[rows], eddt[rows])
-    res["ddt_bias"] = (ddt[rows].sum(0), (eddt + tok_sum * addt)[rows].sum(0))
+    res.update(dx=(gx[rows], err["dx"][rows]), dBm=(gB[rows], err["dBm"][rows]), dCm=(gC[rows], err["dCm"][rows]),
+               dA=(gA, err["dA"]), dD=(gD, err["dD"]), dstate0=(gh, err["dstate0"]), ddt=(ddt[rows], err["ddt"][rows]),
+               ddt_bias=(ddt[rows].sum(0), err["ddt_bias"]))
     if z is not None:
         s = torch.sigmoid(z)
-        ds = s * (1 + z * (1 - s))
-        amp = s * (1 + z.abs() * (1 - s))
-        res["dz"] = ((gg * ds)[rows], (k + 32 * U) * (ag * amp)[rows])
+        res["dz"] = ((gg * s * (1 + z * (1 - s)))[rows], err["dz"][rows])
     return res
 
 
-def _abs_decay_grad(absl, sp, go, gf):
-    """Sum over states of |A| dL/d(delta A) per token, for the absolute problem; and
-    what fp32 loses of it, and of dA, by flushing: a decay below 2^-126 becomes zero,
-    so the term dh a h_prev that it stands in, with h_prev and dh of any size, loses
-    at most 2^-126 |dh h_prev| (times |A|, or times delta)."""
-    x, sa, sb, A, Bm, Cm, Dk, gate, h0 = [t.detach() for t in absl]
+def _scan_errors(x, raw, step, slope, A, Bm, Cm, Dskip, z, gate, h0, sp, softplus, go, gf):
+    """dict name -> slack of ``scan``: an fp32 evaluation's errors carried along token by token, to first order (1 % on
+    top for the rest) and at their worst, never with one token's or state's numbers for another's. Relative errors,
+    in U:
+      step      the sum with the bias is rounded once, which moves softplus by |raw| at raw < 0 (slope <= softplus) and
+                by 1 above; its exponential is within 4, 1.3 |raw| for the exponent's product on top; 4 for the
+                logarithm's polynomial and sums. 9 + 2.5 max(-raw, 0) in all. A plain step: 1.
+      decay     the power of two 4, its raised exponent 0.3; the exponent delta A is off by the step's error, log2(e)
+                and two products (2.3), and 4 more where the steps of a tile are summed up first; replacing a tile's
+                product of decays takes another product per decay. 6 + |delta A| (step + 6.5). A decay below 2^-126
+                may become 0.
+      state     two roundings per token (the sum, a tile's correction); an input delta x B: step + 2
+      gate      sigmoid 7 (an exponential 2, a sum, a quotient 4; approximated 1.3 |z| more) and two products
+    A sum of n terms is off by n U of their absolute values."""
     D, N = A.shape
-    rep = D // Bm.shape[1]
+    G = Bm.shape[1]
+    rep = D // G
+    n_tok, S = x.shape[0], len(sp)
+    lens = torch.tensor([e - a for a, e in sp], dtype=torch.long)
+    L = int(lens.max()) if S else 0
     tiny = torch.finfo(torch.float32).tiny
-    res, flush, flush_A = torch.zeros_like(sa), torch.zeros_like(sa), torch.zeros_like(A)
-    row = 0
-    for n, (a, e) in enumerate(sp):
-        h, hs = h0[n], []
-        dec = [torch.exp(sa[t][:, None] * A) for t in range(a, e)]
-        for i, t in enumerate(range(a, e)):
-            hs.append(h)
-            h = dec[i] * h + (sb[t] * x[t])[:, None] * Bm[t].repeat_interleave(rep, 0)
-        q = gf[n]
-        for i in range(e - a - 1, -1, -1):
-            q = q + Cm[a + i].repeat_interleave(rep, 0) * (go[row + i] * gate[a + i])[:, None]
-            res[a + i] = (q * dec[i] * hs[i] * A.abs()).sum(-1)
-            flush[a + i] = tiny * (q * hs[i] * A.abs()).sum(-1)
-            flush_A += tiny * q * hs[i] * sa[a + i][:, None].abs()
-            q = q * dec[i]
-        row += e - a
-    return res, flush, flush_A
+    place = torch.arange(L)
+    ok = place[:, None] < lens[None]                                        # [L, S]
+    at = (torch.tensor([a for a, _ in sp], dtype=torch.long)[None] + place[:, None]).clamp(max=max(n_tok - 1, 0))
+    zero = torch.zeros((), dtype=torch.float64)
+    pick = lambda v: torch.where(ok.view(L, S, *[1] * (v.dim() - 1)), v[at] if n_tok else v.new_zeros(L, S, *v.shape[1:]), zero)  # noqa: E731
+
+    def put(v):
+        """[L, S, ...] back on the token axis."""
+        res = v.new_zeros(n_tok, *v.shape[2:])
+        if n_tok:
+            res[at[ok]] = v[ok]
+        return res
+
+    spread = lambda v: v.repeat_interleave(rep, 2)  # noqa: E731
+    X, St, Sl, Ga = pick(x), pick(step), pick(slope), pick(gate)
+    B, C = pick(Bm), pick(Cm)
+    e_st = pick((9 + 2.5 * (-raw).clamp(min=0)) * U) if softplus else torch.full_like(St, U)
+    e_g = (9 + 1.3 * pick(z).abs()) * U if z is not None else torch.zeros_like(X)
+    da = St[..., None] * A
+    dec = torch.exp(da)
+    e_dec = (6 + 6.5 * da.abs()) * U + da.abs() * e_st[..., None]
+    u = (St * X)[..., None] * spread(B)
+    live = ok[..., None, None]
+
+    h, eh = h0, torch.zeros_like(h0)
+    hs, es, prev, eprev = [], [], [], []
+    for t in range(L):
+        prev.append(h)
+        eprev.append(eh)
+        nh = dec[t] * h + u[t]
+        ne = dec[t] * eh + (e_dec[t] * dec[t] + tiny) * h.abs() + 2 * U * nh.abs() + (e_st[t][..., None] + 2 * U) * u[t].abs()
+        h, eh = torch.where(live[t], nh, h), torch.where(live[t], ne, eh)
+        hs.append(h)
+        es.append(eh)
+    stack = lambda v: torch.stack(v) if L else h0.new_zeros(0, *h0.shape)  # noqa: E731
+    H, E, P, EP = map(stack, (hs, es, prev, eprev))
+    Cd = spread(C)
+    y = (Cd * H).sum(-1) + Dskip * X
+    ey = (Cd.abs() * E).sum(-1) + (N + 6) * U * (Cd * H).abs().sum(-1) + U * (Dskip * X).abs() + U * y.abs()
+    slackened = lambda d: {k: 1.01 * v for k, v in d.items()}  # noqa: E731
+    out = {"out": put(Ga.abs() * ey + (y * Ga).abs() * (e_g + U)), "final": eh}
+    if go is None:
+        return slackened(out)
+
+    Go = pick(go)
+    o, eo = Go * Ga, (Go * Ga).abs() * (e_g + U)
+    q, eq = gf, torch.zeros_like(gf)
+    dh, ed = [None] * L, [None] * L
+    for t in range(L - 1, -1, -1):
+        c = Cd[t] * o[t][..., None]
+        nd = c + q
+        ne = eq + Cd[t].abs() * eo[t][..., None] + 2 * U * c.abs() + U * nd.abs()
+        nq = dec[t] * nd
+        nqe = dec[t] * ne + (e_dec[t] * dec[t] + tiny) * nd.abs() + 2 * U * nq.abs()
+        dh[t], ed[t] = nd, ne
+        q, eq = torch.where(live[t], nq, q), torch.where(live[t], nqe, eq)
+    DH, ED = torch.where(live, stack(dh), zero), torch.where(live, stack(ed), zero)
+    Bd = spread(B)
+    du = (Bd * DH).sum(-1)
+    edu = (Bd.abs() * ED).sum(-1) + (N + 6) * U * (Bd * DH).abs().sum(-1)
+    m = DH * dec * P                                                        # dL/d(delta A)
+    em = dec * P.abs() * ED + (dec * DH).abs() * EP + m.abs() * (e_dec + 3 * U) + tiny * (DH * P).abs()
+    vd = (A * m).sum(-1)
+    evd = (A.abs() * em).sum(-1) + (N + 6) * U * (A * m).abs().sum(-1)
+    dd = (du * X + vd) * Sl
+    e_sl = pick((9 + 2.5 * raw.abs()) * U) if softplus else torch.zeros_like(Sl)
+    edd = Sl * (X.abs() * edu + evd + 2 * U * ((du * X).abs() + vd.abs())) + dd.abs() * (e_sl + U)
+    # sums over channels: lanes, then the channel tiles; over tokens: a thread's of every tile, warps, sequences
+    over = lambda v: v.unflatten(2, (G, rep)).sum(3)  # noqa: E731
+    chans, colsum = (rep / 8 + 8) * U, S / 32 + 33
+    sx = (St * X)[..., None]
+    tiles, toks = (L / 16 + 16 + colsum) * U, (L / 2 + 16 + colsum) * U
+    out.update(
+        dx=put(St * edu + (du * St).abs() * (e_st + 2 * U) + (Dskip.abs() * eo) + 2 * U * (Dskip * o).abs()),
+        dBm=put(over(sx.abs() * ED + (DH * sx).abs() * (e_st[..., None] + 2 * U + chans))),
+        dCm=put(over(o.abs()[..., None] * E + eo[..., None] * H.abs() + (o[..., None] * H).abs() * (U + chans))),
+        dA=(St[..., None] * em + (m * St[..., None]).abs() * (e_st[..., None] + U + tiles)).sum((0, 1)),
+        dD=(X.abs() * eo + (X * o).abs() * (U + toks)).sum((0, 1)),
+        dstate0=eq, ddt=put(edd), ddt_bias=(edd + toks * dd.abs()).sum((0, 1)))
+    if z is not None:
+        Z = pick(z)
+        s = torch.sigmoid(Z)
+        ds = s * (1 + Z * (1 - s))
+        out["dz"] = put((Go * ds).abs() * ey + (Go * y).abs() * ((18 + 3 * Z.abs()) * U * s * (1 + Z.abs()) + 3 * U * ds.abs()))
+    return slackened(out)
 
 
 # ---- layer norm -----------------------------------------------------------------------
