@@ -320,6 +320,7 @@ struct SsmArgs {
     float *dA, *dDskip, *ddt_bias, *dstate0;
     float *part_bc;    // [tiles][2][N][ntok]
     int *status;       // the library's device status word
+    unsigned long long first_tag;     // the first tile's number beside its words; another one withholds them (test switch)
     int mode_x, mode_b, mode_s;  // how rows of x, dt, z (dout), of B, C, and of states are copied
     float *part_par;   // [nseq][D*N of dA, then D of dDskip, then D of ddt_bias]
 };

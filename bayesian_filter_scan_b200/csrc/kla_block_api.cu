@@ -6,6 +6,7 @@
 // Launches: every forward and step call is one kernel; kla_conv_backward two
 // (three with dstate0), kla_layernorm_backward two, kla_ssm_backward three (four
 // without recorded states). Nothing allocates, nothing synchronises.
+#include <cstdlib>
 #include <cstring>
 
 #include "kla_block.cuh"
@@ -146,6 +147,13 @@ kla_status ssm_args(const kla_ssm_desc *d, SsmArgs &g, size_t &es, bool step) {
     g.softplus = d->softplus != 0;
     g.zero_rest = d->zero_rest != 0;
     return KLA_OK;
+}
+
+// What the scan's kernels need where a wait runs out; the test switch lets the first one do.
+bool ssm_waits(SsmArgs &g) {
+    const char *s = getenv("KLA_TEST_WITHHOLD_TILES");
+    g.first_tag = s && *s && *s != '0' ? 0xffffffff00000000ull : 0;
+    return (g.status = status_ptr()) != nullptr;
 }
 
 size_t ssm_state_records(const SsmArgs &g) {
@@ -303,7 +311,7 @@ kla_status kla_ssm_forward(const kla_ssm_desc *d, const void *x, const void *dt,
     b.out(states, ssm_state_records(g), 16, false);
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     if (g.ax.ntok == 0 && !final_state) return KLA_OK;
-    if (!(g.status = status_ptr())) return KLA_ERR_CUDA;
+    if (!ssm_waits(g)) return KLA_ERR_CUDA;
     return of_cuda(launch_ssm_forward(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
@@ -351,7 +359,7 @@ kla_status kla_ssm_backward(const kla_ssm_desc *d, const void *x, const void *dt
     char *p = (char *)ws;
     g.part_bc = (float *)(p + w.bc);
     g.part_par = (float *)(p + w.par);
-    if (!(g.status = status_ptr())) return KLA_ERR_CUDA;
+    if (!ssm_waits(g)) return KLA_ERR_CUDA;
     if (states) {
         g.states = const_cast<float *>(states);
     } else {

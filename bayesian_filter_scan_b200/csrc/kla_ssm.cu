@@ -201,9 +201,12 @@ struct FwdSmem {
 };
 
 constexpr int kSmemLimit = 227 * 1024;
-constexpr unsigned kSpinLimit = 1u << 24;     // polls of a word before a warp gives up (about a second)
 
 constexpr int kRestBlocks = 64;      // CTAs that clear the rows of no sequence
+
+// Polls of a word before a warp gives up, about a second. (Read from the arguments, so that
+// a test could shorten it, it cost one row of 131072 tokens 14 %: other registers.)
+constexpr unsigned kSpinLimit = 1u << 24;
 
 // OUT: writes out (else only states: the walk before a backward pass without
 // recorded states). WIDE: all rows are copied in the widest pieces. blockDim is (32, warps).
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsig
         sA[n * CB + j] = a;
         // tile 0's words are the initial state; the others' carry no tile's number yet
         for (int w = 0; w < warps; ++w)
-            words_of(w)[n * CB + j] = w ? 0xffffffff00000000ull : (unsigned long long)__float_as_uint(h);
+            words_of(w)[n * CB + j] = w ? 0xffffffff00000000ull : g.first_tag | __float_as_uint(h);
     }
     __syncthreads();
     int rh = 0, half = 0;      // the stages of rows and of B and C in use
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
         }
         sA[n * CB + j] = a;
         for (int w = 0; w < warps; ++w) {
-            words_of(w)[n * CB + j] = w ? 0xffffffff00000000ull : (unsigned long long)__float_as_uint(q);
+            words_of(w)[n * CB + j] = w ? 0xffffffff00000000ull : g.first_tag | __float_as_uint(q);
             sums_of(w)[n * CB + j] = 0.f;
         }
     }
@@ -640,6 +643,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                     if (++spin > kSpinLimit) {
                         if (lane == 0) atomicOr(g.status, kStatusTimeout);
                         cp_async_wait();
+                        __syncthreads();    // the one behind the tiles, where the others may stand
                         return;
                     }
                 }

@@ -438,8 +438,9 @@ kla_status kla_layernorm_backward(const kla_norm_desc *desc, const void *x, cons
  * word on the current device: KLA_OK, KLA_ERR_RANGE or KLA_ERR_TIMEOUT from any
  * kernel that ran since the last check, or KLA_ERR_CUDA if the stream failed.
  * (The environment variable KLA_TEST_WITHHOLD_TILES=1, read at each launch of the
- * tensor-core walk, withholds its tile loads so that its first bounded wait runs
- * out: a test switch for this status path, off unless set.) */
+ * tensor-core walk and of the selective scan, withholds the walk's tile loads, or
+ * the scan's first states, so that the first bounded wait runs out: a test switch
+ * for this status path, off unless set.) */
 kla_status kla_check(cudaStream_t stream);
 
 /* Static description of an error code. */

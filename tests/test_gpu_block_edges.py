@@ -170,3 +170,31 @@ def test_one_decay(N, lo, hi):
     near(fin, want, (4 + 2.3 * x.abs()) * ob.U * want, "prompt")
     kla.ssm_step(one, d, A, bc, bc, state, softplus=False)
     near(state, want, (1.2 + 2.3 * x.abs()) * ob.U * want, "step")
+
+
+# ---- waits that run out ----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_bounded_waits_of_the_scan_report_timeout(monkeypatch, dtype):
+    """With the first tile's states withheld each kernel's wait gives up, the status says so, and the context works on."""
+    g = torch.Generator().manual_seed(1)
+    D, N, T = 40, 16, 200
+    x = torch.randn(T, D, generator=g).to(DT[dtype]).cuda()
+    bc = torch.randn(T, 1, N, generator=g).to(DT[dtype]).cuda()
+    A = -torch.rand(D, N, generator=g).cuda()
+    args = (x, x, A, bc, bc)
+    want, states = kla.ssm_forward(*args, z=x, save_states=True)
+    grads = kla.ssm_backward(*args, x, z=x, states=states)
+    kla.check()
+    for call in (lambda: kla.ssm_forward(*args, z=x), lambda: kla.ssm_backward(*args, x, z=x, states=states),
+                 lambda: kla.ssm_backward(*args, x)):
+        monkeypatch.setenv("KLA_TEST_WITHHOLD_TILES", "1")
+        call()
+        with pytest.raises(kla.KlaError) as e:
+            kla.check()
+        assert e.value.status == kla.KLA_ERR_TIMEOUT
+        monkeypatch.delenv("KLA_TEST_WITHHOLD_TILES")
+        out = kla.ssm_forward(*args, z=x)
+        again = kla.ssm_backward(*args, x, z=x, states=states)
+        kla.check()
+        assert torch.equal(out, want) and all(torch.equal(again[k], grads[k]) for k in grads)
