@@ -160,8 +160,7 @@ __device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
 // bf16, whose steps are known to 2^-9, y comes from the approximated power of two, whose
 // rounded exponent makes it |x| 2^-24 off (relative; 1e-6 at x = -12).
 template <typename T>
-__device__ __forceinline__ void softplus2(float &x0, float &x1) {
-    f32x2 y;
+__device__ __forceinline__ void softplus2(float &x0, float &x1, f32x2 &y) {
     if constexpr (sizeof(T) == 4) y = pack2(expf(-fabsf(x0)), expf(-fabsf(x1)));
     else y = pack2(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
     f32x2 p = dup2(-0.0033065395f);
@@ -179,6 +178,19 @@ __device__ __forceinline__ void softplus2(float &x0, float &x1) {
     x0 = m0;
     x1 = m1;
 }
+template <typename T>
+__device__ __forceinline__ void softplus2(float &x0, float &x1) {
+    f32x2 y;
+    softplus2<T>(x0, x1, y);
+}
+// The slope of softplus at x, sigmoid(x), from the y = e^-|x| that softplus2 leaves.
+template <typename T>
+__device__ __forceinline__ float softplus_slope(float x, float y) {
+    const float n = x < 0.f ? y : 1.f;
+    if constexpr (sizeof(T) == 4) return __fdividef(n, 1.f + y);
+    return n * rcp(1.f + y);
+}
+
 // V floats as pairs (the last one alone when V is 1).
 template <int V>
 struct Pairs {

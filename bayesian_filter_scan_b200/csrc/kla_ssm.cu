@@ -721,8 +721,14 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
         const int mine_n = live ? have - ls * LS : 0;
 #pragma unroll
         for (int i = 0; i < LS; i += 2) {
-            float st[2] = {rs[i], rs[i + 1]};
-            if (g.softplus) softplus2<T>(st[0], st[1]);
+            float st[2] = {rs[i], rs[i + 1]}, slope[2] = {1.f, 1.f};
+            if (g.softplus) {
+                f32x2 e;
+                softplus2<T>(st[0], st[1], e);
+                unpack2(e, slope[0], slope[1]);
+                slope[0] = softplus_slope<T>(rs[i], slope[0]);
+                slope[1] = softplus_slope<T>(rs[i + 1], slope[1]);
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int j = i + k;
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(256) ssm_backward_kernel(const SsmArgs g) {
                     dz = o * full * sg * fmaf(zs[j], 1.f - sg, 1.f);
                     o *= zs[j] * sg;
                 }
-                const float dd = fmaf(vu[j], xs[j], vd[j]) * (g.softplus ? sigmoid_for<T>(rs[j]) : 1.f);
+                const float dd = fmaf(vu[j], xs[j], vd[j]) * slope[k];
                 if (j < mine_n) {
                     const long long at = row + (long long)j * g.D;
                     static_cast<T *>(g.dx)[at] = from_f<T>(fmaf(vu[j], st[k], skip * o));
