@@ -198,3 +198,100 @@ def test_bounded_waits_of_the_scan_report_timeout(monkeypatch, dtype):
         again = kla.ssm_backward(*args, x, z=x, states=states)
         kla.check()
         assert torch.equal(out, want) and all(torch.equal(again[k], grads[k]) for k in grads)
+
+
+# ---- single tokens in a graph -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,B,D,N", [("bf16", 1, 64, 16), ("fp32", 9, 40, 20), ("bf16", 70, 128, 16), ("fp32", 3, 7, 5)])
+def test_captured_single_tokens_follow_eager_ones(dtype, B, D, N):
+    """A decoding step's two calls, captured on another stream and replayed token by token on states that change in
+    place, leave bit for bit what eager calls leave."""
+    g = torch.Generator().manual_seed(B + D)
+    t = DT[dtype]
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    tokens = [[v.to(t).cuda() for v in (r(B, D), r(B, D), r(B, D), r(B, 1, N), r(B, 1, N))] for _ in range(7)]
+    w, b, A, Dk = r(D, 4).cuda(), r(D).cuda(), -torch.rand(D, N, generator=g).cuda(), r(D).cuda()
+    hist0, state0 = r(B, 3, D).to(t).cuda(), r(B, D, N).cuda()
+
+    def step(tok, hist, state):
+        x, dt, z, Bm, Cm = tok
+        return kla.ssm_step(kla.conv_step(x, w, hist, b), dt, A, Bm, Cm, state, D=Dk, z=z)
+
+    hist, state = hist0.clone(), state0.clone()
+    want = [step(tok, hist, state) for tok in tokens]
+    mine, mh, ms = [v.clone() for v in tokens[0]], hist0.clone(), state0.clone()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(mine, mh.clone(), ms.clone())
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(mine, mh, ms)
+    torch.cuda.synchronize()
+    for _ in range(2):      # the second time around from the first states again
+        mh.copy_(hist0)
+        ms.copy_(state0)
+        for tok, exp in zip(tokens, want):
+            for m, v in zip(mine, tok):
+                m.copy_(v)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, exp)
+        assert torch.equal(mh, hist) and torch.equal(ms, state)
+
+
+# ---- around the Kalman mixer -------------------------------------------------------------
+
+def test_convolution_and_norm_around_the_kalman_mixer():
+    """q, k, v through the block's convolution, the Kalman mixer, and a norm of every head's output: forward and
+    gradients against the formulas in 64 bits. The bar is that of the mixer's own gradients, 2e-3 of the largest
+    value (fp32 sums along the rows); the operators around it add some hundred roundings, 2^-24 each."""
+    B, T, H, dk, dv, W = 2, 45, 2, 16, 32, 4
+    n = B * T
+    g = torch.Generator().manual_seed(5)
+    r = lambda *s, sc=1.0: sc * torch.randn(*s, generator=g)  # noqa: E731
+    x = {"q": r(n, H * dk), "k": r(n, H * dk), "v": r(n, H * dv)}
+    w = {"q": r(H * dk, W, sc=0.5), "k": r(H * dk, W, sc=0.5), "v": r(H * dv, W, sc=0.5)}
+    bias = {k: r(v.shape[1], sc=0.1) for k, v in x.items()}
+    a, qn, beta = torch.sigmoid(r(n, H, dk) + 2), 0.1 * torch.rand(n, H, dk, generator=g), torch.sigmoid(r(n, H))
+    lw, lb, dout = 1 + r(dv, sc=0.1), r(dv, sc=0.1), r(n * H, dv)
+    c = lambda t: t.cuda()  # noqa: E731
+    kw = dict(B=B, T=T)
+
+    conv = {k: kla.conv_forward(c(x[k]), c(w[k]), c(bias[k]), **kw) for k in x}
+    heads = {k: v.view(n, H, -1) for k, v in conv.items()}
+    gates = (c(a), c(qn), c(beta))
+    mix = kla.forward(heads["q"], heads["k"], heads["v"], *gates, **kw)
+    y, mean, rstd = kla.layernorm_forward(mix.view(n * H, dv), c(lw), c(lb), stats=True)
+    ln = kla.layernorm_backward(mix.view(n * H, dv), c(dout), mean, rstd, c(lw))
+    mg = kla.backward(heads["q"], heads["k"], heads["v"], *gates, ln["dx"].view(n, H, dv), **kw)
+    got = {"y": y, "lw": ln["dweight"], "lb": ln["dbias"], "a": mg["da"], "beta": mg["dbeta"]}
+    for k in x:
+        cg = kla.conv_backward(c(x[k]), c(w[k]), mg["d" + k].view(n, -1), c(bias[k]), **kw)
+        got.update({"x" + k: cg["dx"], "w" + k: cg["dweight"], "b" + k: cg["dbias"]})
+    torch.cuda.synchronize()
+    kla.check()
+
+    leaf = {"lw": lw, "lb": lb, "a": a, "beta": beta, **{"x" + k: v for k, v in x.items()},
+            **{"w" + k: v for k, v in w.items()}, **{"b" + k: v for k, v in bias.items()}}
+    leaf = {k: v.double().requires_grad_() for k, v in leaf.items()}
+    sp = ob.spans(0, B=B, T=T)
+    q, k, v = (ob._conv_rows(leaf["x" + i], leaf["w" + i], leaf["b" + i],
+                             torch.zeros(B, W - 1, x[i].shape[1], dtype=torch.float64), sp, True)[0].view(n, H, -1)
+               for i in "qkv")
+    outs, qd = [], qn.double()
+    for s, e in sp:
+        lam, eta = torch.ones(H, dk, dtype=torch.float64), torch.zeros(H, dk, dv, dtype=torch.float64)
+        for t in range(s, e):
+            den = leaf["a"][t] ** 2 + qd[t] * lam
+            bk = leaf["beta"][t][:, None] * k[t]
+            eta = (leaf["a"][t] / den)[..., None] * eta + bk[..., None] * v[t][:, None, :]
+            lam = lam / den + bk * k[t]
+            outs.append(((q[t] / lam)[..., None] * eta).sum(1))
+    m = torch.stack(outs).view(n * H, dv)
+    mu = m.mean(1, keepdim=True)
+    want = (m - mu) * (((m - mu) ** 2).mean(1, keepdim=True) + 1e-5).rsqrt() * leaf["lw"] + leaf["lb"]
+    grads = torch.autograd.grad(want, list(leaf.values()), dout.double())
+    for name, exp in [("y", want.detach())] + list(zip(leaf, grads)):
+        err = (got[name].double().cpu() - exp).abs().max() / exp.abs().max()
+        assert err <= 2e-3, (name, float(err))
