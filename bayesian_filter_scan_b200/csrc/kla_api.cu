@@ -207,7 +207,7 @@ const char *kla_status_string(kla_status s) {
     return "unknown status";
 }
 
-int kla_version(void) { return 100; }
+int kla_version(void) { return 200; }
 
 size_t kla_workspace_bytes(const kla_desc *d) {
     Plan p;

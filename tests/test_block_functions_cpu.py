@@ -1,11 +1,13 @@
 """The polynomials of the recurrent block's kernels, from the coefficients that the
 sources hold, in fp64: within the errors that the sources state."""
+import ctypes
 import os
 import re
 
 import numpy as np
 
 from bayesian_filter_scan_b200 import build as kbuild
+from bayesian_filter_scan_b200 import kla
 
 
 def coefficients(source, function):
@@ -39,3 +41,15 @@ def test_power_of_two_polynomial():
     assert len(c) == 7
     f = np.linspace(-0.5, 0.5, 100001)
     check(c, f, np.exp2(f), 3.0e-9)
+
+
+def test_constants_of_the_binding_are_the_librarys():
+    kbuild.build()
+    L = kla.lib()
+
+    def nbytes(T, N):
+        return L.kla_ssm_states_bytes(ctypes.byref(kla.KlaSsmDesc(1, T, 8, 1, N, kla.KLA_FP32, 1, None, 0)))
+
+    assert nbytes(kla.SSM_STATE_EVERY * 3, 4) - nbytes(kla.SSM_STATE_EVERY * 2, 4) == 8 * 4 * 4
+    assert nbytes(kla.SSM_STATE_EVERY * 3 - 1, 4) == nbytes(kla.SSM_STATE_EVERY * 2, 4)
+    assert nbytes(16, kla.SSM_MAX_STATES) > 0 and nbytes(16, kla.SSM_MAX_STATES + 1) == 0
