@@ -303,10 +303,10 @@ struct ConvArgs {
     void *dx, *dstate0;
     float *part;       // [blocks][D*W taps, then D biases]
 };
-cudaError_t launch_conv_forward(const ConvArgs &, bool bf16, cudaStream_t);
+cudaError_t launch_conv_forward(const ConvArgs &, bool bf16, int sms, cudaStream_t);
 int conv_backward_blocks(long long ntok);     // at most
 cudaError_t launch_conv_backward(const ConvArgs &, bool bf16, int sms, float *dweight, float *dbias, cudaStream_t);
-cudaError_t launch_conv_step(const ConvArgs &, bool bf16, cudaStream_t);
+cudaError_t launch_conv_step(const ConvArgs &, bool bf16, int sms, cudaStream_t);
 
 constexpr int kSsmCkpt = 16;      // tokens between two recorded states of a sequence
 constexpr int kSsmMaxN = 128;

@@ -229,7 +229,7 @@ kla_status kla_conv_forward(const kla_conv_desc *d, const void *x, const float *
     b.out(final_state, hist, es, false);
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     g.x = x; g.w = weight; g.bias = bias; g.state0 = state0; g.out = out; g.final_state = final_state;
-    return of_cuda(launch_conv_forward(g, d->dtype == KLA_BF16, st));
+    return of_cuda(launch_conv_forward(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
 size_t kla_conv_backward_workspace_bytes(const kla_conv_desc *d) {
@@ -283,7 +283,7 @@ kla_status kla_conv_step(const kla_conv_desc *d, const void *x, const float *wei
     b.out(out, (size_t)g.ax.ntok * g.D * es, es);
     if (!b.good()) return KLA_ERR_INVALID_ARG;
     g.x = x; g.w = weight; g.bias = bias; g.final_state = state; g.out = out;
-    return of_cuda(launch_conv_step(g, d->dtype == KLA_BF16, st));
+    return of_cuda(launch_conv_step(g, d->dtype == KLA_BF16, sm_count(), st));
 }
 
 size_t kla_ssm_states_bytes(const kla_ssm_desc *d) {

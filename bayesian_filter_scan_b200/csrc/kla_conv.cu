@@ -418,7 +418,7 @@ bool rows_aligned(const ConvArgs &g, int es, size_t a) {
 }
 
 template <int W, int V, int BATCH, typename T>
-cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
+cudaError_t forward_t(const ConvArgs &g, int sms, cudaStream_t st) {
     const int nvec = (g.D + V - 1) / V;
     int bx = 1;
     while (bx < nvec && bx < kConvThreads) bx *= 2;
@@ -426,7 +426,7 @@ cudaError_t forward_t(const ConvArgs &g, cudaStream_t st) {
     // long runs load the taps, the rows in front of them and their sequence's offsets less
     // often; short ones fill the SMs
     int run = 64;
-    while (run > BATCH && nvec * (g.ax.ntok / run) < 148LL * 1024) run /= 2;
+    while (run > BATCH && nvec * (g.ax.ntok / run) < sms * 1024LL) run /= 2;
     const long long tok_blocks = (g.ax.ntok + (long long)runs * run - 1) / ((long long)runs * run);
     const long long seq_blocks = (W > 1 && g.final_state) ? (g.ax.nseq + runs - 1) / runs : 0;
     const long long rest_blocks = g.zero_rest && g.ax.cu ? (tok_blocks < 64 ? tok_blocks : 64) : 0;
@@ -464,10 +464,10 @@ cudaError_t backward_t(const ConvArgs &g, int sms, int &blocks, cudaStream_t st)
 }
 
 template <int W, int V, typename T>
-cudaError_t step_t(const ConvArgs &g, cudaStream_t st) {
+cudaError_t step_t(const ConvArgs &g, int sms, cudaStream_t st) {
     const int nvec = (g.D + V - 1) / V;
     int run = 8;
-    while (run > 1 && (long long)nvec * (g.ax.nseq / run) < 148LL * 256) run /= 2;
+    while (run > 1 && (long long)nvec * (g.ax.nseq / run) < sms * 256LL) run /= 2;
     const long long n = (long long)nvec * ((g.ax.nseq + run - 1) / run), blocks = (n + kConvThreads - 1) / kConvThreads;
     if (!blocks) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -483,8 +483,8 @@ cudaError_t conv_w(const ConvArgs &g, Call call, int sms, int &blocks, cudaStrea
     const bool vec = rows_aligned(g, sizeof(T), 8);
     // 8-byte accesses, four rows ahead: 80 registers (32768 tokens of 2048 channels 70 us;
     // 78 eight rows ahead, 85 and 93 with 16-byte accesses, whose registers halve the warps)
-    if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, st) : forward_t<W, 1, 8, T>(g, st);
-    if (call == Call::kStep) return vec ? step_t<W, V / 2, T>(g, st) : step_t<W, 1, T>(g, st);
+    if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, sms, st) : forward_t<W, 1, 8, T>(g, sms, st);
+    if (call == Call::kStep) return vec ? step_t<W, V / 2, T>(g, sms, st) : step_t<W, 1, T>(g, sms, st);
     // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers
     return vec ? backward_t<W, V / 2, T>(g, sms, blocks, st) : backward_t<W, 1, T>(g, sms, blocks, st);
 }
@@ -505,9 +505,9 @@ cudaError_t conv_any(const ConvArgs &g, bool bf16, Call call, int sms, int &bloc
 
 }  // namespace
 
-cudaError_t launch_conv_forward(const ConvArgs &g, bool bf16, cudaStream_t st) {
+cudaError_t launch_conv_forward(const ConvArgs &g, bool bf16, int sms, cudaStream_t st) {
     int none = 0;
-    return conv_any(g, bf16, Call::kForward, 0, none, st);
+    return conv_any(g, bf16, Call::kForward, sms, none, st);
 }
 
 int conv_backward_blocks(long long ntok) {
@@ -522,9 +522,9 @@ cudaError_t launch_conv_backward(const ConvArgs &g, bool bf16, int sms, float *d
                          st);
 }
 
-cudaError_t launch_conv_step(const ConvArgs &g, bool bf16, cudaStream_t st) {
+cudaError_t launch_conv_step(const ConvArgs &g, bool bf16, int sms, cudaStream_t st) {
     int none = 0;
-    return conv_any(g, bf16, Call::kStep, 0, none, st);
+    return conv_any(g, bf16, Call::kStep, sms, none, st);
 }
 
 }  // namespace kla
