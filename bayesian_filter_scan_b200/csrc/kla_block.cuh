@@ -98,6 +98,19 @@ __device__ __forceinline__ void store_v(T *p, const float (&x)[V]) {
     }
 }
 
+// Clears n elements at p with `threads` threads, 16 bytes at a time where they go. A call:
+// in line it changed the schedule of the scan's kernel around it (one row of 131072 tokens
+// 2.54 ms, 2.45 with the call).
+template <typename T>
+__device__ __noinline__ void clear(T *p, long long n, long long tid, long long threads) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const long long front = min(n, (long long)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T));
+    const long long wide = (n - front) / V, back = front + wide * V;
+    for (long long e = tid; e < wide; e += threads)
+        reinterpret_cast<uint4 *>(p + front)[e] = make_uint4(0, 0, 0, 0);
+    for (long long e = tid; e < front + n - back; e += threads) p[e < front ? e : back + e - front] = from_f<T>(0.f);
+}
+
 // Sigmoid through the accurate exponential and an approximate quotient (2 units in
 // the last place); 0 where the exponential overflows.
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + expf(-x)); }

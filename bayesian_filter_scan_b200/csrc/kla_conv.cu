@@ -68,17 +68,17 @@ template <int W, int V, int BATCH, typename T>
 __global__ void __launch_bounds__(kConvThreads) conv_forward_kernel(const ConvArgs g, int bx, int run, long long tok_blocks,
                                                                     long long seq_end) {
     const int cv = blockIdx.y * bx + threadIdx.x % bx, c = cv * V;
-    if (c >= g.D) return;
-    const T *x = static_cast<const T *>(g.x);
     if (blockIdx.x >= seq_end) {
-        const long long step = (gridDim.x - seq_end) * (kConvThreads / bx);
-        const long long from = (blockIdx.x - seq_end) * (kConvThreads / bx) + threadIdx.x / bx;
+        T *out = static_cast<T *>(g.out);
+        const long long step = (gridDim.x - seq_end) * gridDim.y * kConvThreads, D = g.D;
+        const long long from = ((blockIdx.x - seq_end) * gridDim.y + blockIdx.y) * kConvThreads + threadIdx.x;
         const long long head = min((long long)g.ax.cu[0], g.ax.ntok), tail = max(g.ax.cu[g.ax.nseq], 0);
-        const float zero[V] = {};
-        for (long long t = from; t < head; t += step) store_v<V>(static_cast<T *>(g.out) + t * g.D + c, zero);
-        for (long long t = tail + from; t < g.ax.ntok; t += step) store_v<V>(static_cast<T *>(g.out) + t * g.D + c, zero);
+        if (head > 0) clear(out, head * D, from, step);
+        if (tail < g.ax.ntok) clear(out + tail * D, (g.ax.ntok - tail) * D, from, step);
         return;
     }
+    if (c >= g.D) return;
+    const T *x = static_cast<const T *>(g.x);
     if (blockIdx.x >= tok_blocks) {
         // the last W-1 inputs of one sequence
         if constexpr (W > 1) {

@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(512) ssm_forward_kernel(const SsmArgs g, unsig
         const long long step = (long long)(gridDim.x - units) * warps * 32;
         const long long from = ((long long)(blockIdx.x - units) * warps + warp) * 32 + lane, D = g.D;
         const long long head = min((long long)g.ax.cu[0], g.ax.ntok), tail = max(g.ax.cu[g.ax.nseq], 0);
-        for (long long e = from; e < head * D; e += step) out[e] = from_f<T>(0.f);
-        for (long long e = tail * D + from; e < g.ax.ntok * D; e += step) out[e] = from_f<T>(0.f);
+        if (head > 0) clear(out, head * D, from, step);
+        if (tail < g.ax.ntok) clear(out + tail * D, (g.ax.ntok - tail) * D, from, step);
         return;
     }
     unsigned char *mine = smem + warp * M::warp(g.N);
