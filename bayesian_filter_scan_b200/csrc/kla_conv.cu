@@ -9,9 +9,10 @@
 // registers, so every row is read once, but for the W-1 rows in front of each run; the
 // next rows are on their way meanwhile, and a batch inside one sequence takes a path
 // without its checks. Measured: 32768 packed tokens of 2048 channels in bf16 61 us (4.4
-// TB/s); gradients of 16384 tokens 74 us (2.7 TB/s: the sums per tap and the halo on
-// both sides keep the issue slots busy); rows of odd length, one element per access,
-// take 1.4 times as long.
+// TB/s), in fp32 97 us (5.5 TB/s); gradients of 16384 tokens 74 us (2.7 TB/s: the sums per
+// tap and the halo on both sides keep the issue slots busy), in fp32 93 us (4.3 TB/s); rows
+// of odd length, one element per access, take 1.5 times as long (32768 x 2047 in bf16 92
+// us, gradients 193 us against 136).
 #include "kla_block.cuh"
 
 namespace kla {
@@ -24,8 +25,8 @@ constexpr int kBwdRuns = 8;       // runs per CTA
 constexpr int kBwdBatch = 4;      // rows in flight per thread, backward
 constexpr int kBwdLanes = 32;     // channel vectors per CTA
 
-// Row `back` places before token t of the sequence that starts at s0: x, or the
-// history's row, or 0.
+// The row at place p of sequence n, which starts at s0: x there, or in front of s0 the
+// history's row, or 0 without one.
 template <int W, int V, typename T>
 __device__ __forceinline__ void row_before(const ConvArgs &g, int n, long long s0, long long p, int c,
                                            float (&v)[V]) {
@@ -481,8 +482,9 @@ template <int W, typename T>
 cudaError_t conv_w(const ConvArgs &g, Call call, int sms, int &blocks, cudaStream_t st) {
     constexpr int V = 16 / (int)sizeof(T);
     const bool vec = rows_aligned(g, sizeof(T), 8);
-    // 8-byte accesses, four rows ahead: 80 registers (32768 tokens of 2048 channels 70 us;
-    // 78 eight rows ahead, 85 and 93 with 16-byte accesses, whose registers halve the warps)
+    // 8-byte accesses, four rows ahead: 80 registers. Chosen when 32768 tokens of 2048
+    // channels took 70 us (61 now): 78 eight rows ahead, 85 and 93 with 16-byte accesses,
+    // whose registers halve the warps
     if (call == Call::kForward) return vec ? forward_t<W, V / 2, 4, T>(g, sms, st) : forward_t<W, 1, 8, T>(g, sms, st);
     if (call == Call::kStep) return vec ? step_t<W, V / 2, T>(g, sms, st) : step_t<W, 1, T>(g, sms, st);
     // backward: 8-byte accesses, whose taps, windows and sums of W rows still fit in registers

@@ -147,9 +147,10 @@ __device__ __forceinline__ float mob_apply(const Mob &M, float x) {
     return fmaf(M.m00, x, M.m01) / fmaf(M.m10, x, M.m11);
 }
 
-// Programmatic dependent launch. Every kernel of the library is launched with
-// programmatic stream serialization, so it may start while the kernel before
-// it in the stream is still running. Each kernel therefore
+// Programmatic dependent launch. Every kernel of the filter (all but those of the
+// recurrent block, kla_block.cuh, whose plain launches wait for the whole grid
+// before them) is launched with programmatic stream serialization, so it may start
+// while the kernel before it in the stream is still running. Each therefore
 //  * calls pdl_wait() before its first global-memory access (read or write):
 //    it returns once the preceding grid has completed and its writes are
 //    visible, so the data dependences are those of plain stream order;

@@ -7,8 +7,13 @@
 // passes (mean, then squared deviations from it, then the result), so it is read
 // once; the variance is the mean of squared deviations, which loses nothing when
 // the mean is large. Measured in bf16: the norm of a residual sum, 32768 rows of 2048
-// (two tensors in, two out), 108 us (5.0 TB/s); 524288 rows of 128 forward 61 us (4.4
-// TB/s), backward 80 us (5.0 TB/s).
+// (two tensors in, two out), 105 us (5.1 TB/s); 524288 rows of 128 forward 60 us (4.5
+// TB/s), backward 79 us (5.1 TB/s); in fp32 212, 109 and 144 us (5.1, 4.9 and 5.6 TB/s).
+// Rows that are no multiple of 16 bytes go one value per access, and a thread holds up to
+// 64 of them: 128 to 255 registers, and spills from 8193 values on. A residual sum of 2^26
+// values in bf16, forward and backward: rows of 2047 198 and 508 us, 4099 448 and 827, 8191
+// 261 and 680, 16383 1650 and 1404, against 104 and 105 (2048), 97 and 98 (4096), 109 and
+// 122 (8192), 123 and 266 (16384). fp32 rows of 16384, which spill too, 269 and 857.
 #include "kla_block.cuh"
 
 namespace kla {
@@ -310,7 +315,8 @@ void spread(int nvec, int most, int threads, int &lanes, int &warps) {
 template <int V, int NV, typename T>
 cudaError_t fwd(const NormArgs &g, int lanes, int warps, int sms, cudaStream_t st) {
     const int rows = kNormThreads / (lanes * warps);
-    // four CTAs of 64 registers a thread fit on an SM
+    // four CTAs of 64 registers a thread fit on an SM (rows on 16 bytes of up to 2048 values
+    // in bf16, 1024 in fp32); of the wider variants one or two, in as many more waves
     const long long blocks = (g.rows + rows - 1) / rows, most = 4LL * sms;
     norm_forward_kernel<V, NV, T><<<(unsigned)(blocks < most ? blocks : most), kNormThreads, 0, st>>>(g, lanes, warps);
     return cudaGetLastError();
@@ -369,7 +375,8 @@ cudaError_t launch_norm_forward(const NormArgs &g, bool bf16, int sms, cudaStrea
 
 int norm_backward_ctas(long long rows, int D, int sms) {
     // rows a CTA has in flight (for the vectorised form); two CTAs of 111 registers a
-    // thread fit on an SM (524288 rows of 128: 80 us, 98 with three, 82 with four)
+    // thread fit on an SM (524288 rows of 128: 80 us, 98 with three, 82 with four); of the
+    // variants with 184 registers and more, or 512 threads, one
     int per = kNormThreads * 8 * 2 / (D < 8 ? 8 : D);
     if (per < 1) per = 1;
     const long long want = (rows + per - 1) / per, most = 2LL * sms;

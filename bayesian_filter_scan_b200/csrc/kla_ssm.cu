@@ -20,8 +20,8 @@
 // reader hands on. A tile's steps, inputs and outputs stay in registers, as pairs of
 // tokens for the packed fp32 instructions; its rows arrive by asynchronous copies while
 // the tile before is worked on.
-// Measured, bf16, 2048 channels, 16 states: 8 rows of 4096 tokens 548 us, one row of
-// 131072 tokens 2.44 ms, 4 rows of 2048 with recorded states 174 us. The exponentials
+// Measured, bf16, 2048 channels, 16 states: 8 rows of 4096 tokens 550 us, one row of
+// 131072 tokens 2.45 ms, 4 rows of 2048 with recorded states 174 us (259 in fp32). The exponentials
 // alone are 240 us, 0.96 ms and 60 us; the exponential unit is 48 % busy, the issue
 // slots 53 %: with 16 warps per SM (128 registers a thread) the dependent steps of a
 // tile and the 650 instructions per tile outside its state loop (of 1480) are not
@@ -32,11 +32,12 @@
 // warp walks its tile's states forward and then the adjoint backward with one set of
 // decays. dB and dC are sums over channels: a transposing reduction over the warp's
 // channels leaves each lane one token's sum, and a second kernel adds the channel tiles
-// in a fixed order. Measured: 4 rows of 2048 tokens, 2048 channels, 16 states, 566 us
-// and 25 us for the channel tiles' sums. Eight warps per SM (255 registers) issue in
-// 43 % of the slots, a quarter of the instructions are the two reductions. (Those as
-// tensor-core products with ones: 531 us, but their tf32 operands cut the terms to 11
-// bits. Tiles of 8 tokens, which fit twice the warps: 600 us and twice the states.)
+// in a fixed order. Measured: 4 rows of 2048 tokens, 2048 channels, 16 states, 550 us
+// (fp32 586) and 25 us for the channel tiles' sums. Eight warps per SM (255 registers) issue in
+// 46 % of the slots, a quarter of the instructions are the two reductions. (Those as
+// tensor-core products with ones, when this took 574 us: 531, but their tf32 operands cut
+// the terms to 11 bits. Tiles of 8 tokens, which fit twice the warps: 600 us and twice the
+// states.)
 #include <initializer_list>
 
 #include "kla_block.cuh"
@@ -50,7 +51,12 @@ constexpr int kTileNB = 16;      // states whose B and C a warp stages at once
 constexpr int kLdPad = 4;        // floats behind a state's tokens in shared memory: states on other banks
 
 // How rows reach shared memory: pieces of 16 bytes (or a whole narrower row), of 4
-// bytes, or single elements, by the alignment of the rows.
+// bytes, or single elements, by the alignment of the rows. Elements of bf16 have no
+// asynchronous copy, so a tile waits for its rows. 4 rows of 2048 tokens, 16 states, bf16,
+// forward and backward: 174 and 551 us with 2048 channels, 231 and 651 with 2046 (4 bytes),
+// 334 and 895 with 2047 (elements); 8 rows of 4096 tokens forward 550 and 1250 us with 2048
+// and 2047. An odd number of states does the same to B and C (17 states 381 us, 18 states
+// 319). fp32 rows off 16 bytes: 2047 channels 390 and 719 us, 2048 259 and 586.
 enum : int { kScalar = 0, kWord = 1, kWide = 2 };
 
 template <int B>
@@ -859,10 +865,10 @@ cudaError_t forward_t(const SsmArgs &g, int sms, cudaStream_t st) {
     if (units(8) > 0x7fffffffLL - kRestBlocks) return cudaErrorInvalidValue;
     // 16 channels per CTA, or 8 where that leaves a quarter of the SMs without one (fewer
     // channels split the same rows into more CTAs, but share what every tile costs less:
-    // with 16 and with 8 channels, 4 rows of 2048 tokens of 2048 channels took 177 and 215
-    // us, 12 units of 130 channels 75 and 49). As many warps as fill the SMs' 16: one row of
-    // 131072 tokens of 2048 channels took 6.1, 3.6 and 2.8 ms with 4, 8 and 16 of them, 8
-    // rows of 4096 tokens 600, 586 and 671 us.
+    // with 16 and with 8 channels, 4 rows of 2048 tokens of 2048 channels took 174 and 197
+    // us, 12 units of 130 channels and 64 states, of about 470 fp32 tokens, 70 and 63). As
+    // many warps as fill the SMs' 16: one row of 131072 tokens of 2048 channels took 5.1,
+    // 3.2 and 2.4 ms with 4, 8 and 16 of them, 8 rows of 4096 tokens 558, 547 and 585 us.
     const bool wide = 4 * units(16) >= 3LL * sms;
     const long long n = wide ? units(16) : units(8);
     // Packed sequences are uneven, and the longest is the last to end: 16 there.
@@ -880,8 +886,8 @@ cudaError_t backward_cb(SsmArgs g, int sms, cudaStream_t st) {
     const long long units = (long long)g.ax.nseq * tiles;
     if (units > 0x7fffffffLL) return cudaErrorInvalidValue;
     // two CTAs of four warps fill an SM's registers (255 of a thread: the tile's six
-    // arrays and a state's decays and walk stand in them; 168 cost spills and 855 us for
-    // 4 x 2048 tokens of 2048 channels against 574); eight warps where CTAs are few
+    // arrays and a state's decays and walk stand in them; 168 cost spills and 1011 us for
+    // 4 x 2048 tokens of 2048 channels against 551); eight warps where CTAs are few
     int warps = units > 2LL * sms ? 4 : 8;
     while (warps > 1 && M::bytes(g.N, warps) > (size_t)kSmemLimit) --warps;
     g.mode_x = copy_mode({{g.x, g.ld_x}, {g.dt, g.ld_dt}, {g.z, g.ld_z}, {g.dout, g.D}}, g.D / g.G, sizeof(T),
